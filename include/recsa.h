@@ -336,6 +336,124 @@ RECSA_API recsa_status recsa_tree_set_offload_staging(recsa_tree* tree, void* st
 /* Free the host handle.  Device memory stays with the caller. */
 RECSA_API recsa_status recsa_tree_free(recsa_tree* tree);
 
+/* ---------------------------------------------------------------------------------
+ * A KV cache held in 4 bits: write, attention for single tokens and chunks, eviction by
+ * accumulated attention weight.  It stands beside the tree for layers that attend to
+ * their whole cache, or to a bounded part of it: at d = 128 a token takes 160 bytes a KV
+ * head (512 in bf16).  The pages have no counterpart.
+ *
+ * A row (one token's key or value of one KV head) is held in groups of 32 dims.  For the
+ * group's elements x:
+ *   lo   = the largest bf16 <= min(x);   s = the smallest bf16 >= (max(x) - lo) / 15;
+ *   code = (x - lo) / s to the nearest integer, ties to even (0 if s = 0);
+ *   value = lo + s * code, in fp32 arithmetic, rounded once to the storage dtype where
+ *   it is read back.  Attention uses these values.
+ * A group with a NaN or an infinity, or whose lo or s is no finite bf16, reads back as
+ * NaN in all its dims; attention over such a token is NaN for the rows that see it and
+ * unchanged for the rows that do not.
+ *
+ * A slot is a row's place in the cache, a position the number of tokens appended before
+ * it.  They are the same until recsa_kv4_evict moves a row.  Keys carry no rotation of
+ * the library's: a caller whose model rotates q and k does so before both.
+ *
+ * recsa_config: head_dim, n_q_heads, n_kv_heads, dtype and scale are used; C, k,
+ * rope_base and pooler_w are not read.  Errors and streams are as for the tree: calls
+ * are asynchronous on their stream, can be captured in CUDA graphs, check arguments on
+ * the host, and record what only the device sees (a length past the capacity, a count
+ * out of range) in a sticky status word.  Calls on one handle share its workspace: they
+ * must not overlap on the GPU, and neither may two graphs that hold them.  A call may be
+ * made while another device than the cache's is current; the stream belongs to the
+ * cache's device. */
+typedef struct recsa_kv4 recsa_kv4;     /* opaque host handle; does not own device memory */
+
+/* Sizes of the caller's buffers for `capacity` tokens a sequence (at most 2^30),
+ * `batch` sequences and waves of at most `max_queries` query rows (>= batch; a chunk is
+ * processed in waves of max_queries / batch rows of every sequence).  Errors:
+ * RECSA_E_INVAL, RECSA_E_UNSUPPORTED (head_dim, group size, batch * n_kv_heads > 65535). */
+RECSA_API recsa_status recsa_kv4_query_sizes(const recsa_config* cfg, int64_t capacity,
+                                             int32_t batch, int32_t max_queries,
+                                             size_t* cache_bytes, size_t* workspace_bytes);
+
+/* Bind a cache to caller memory (device memory, 256-byte aligned) and empty it on
+ * `stream`: lengths, positions and weights 0.  On success *out receives a new handle
+ * (free with recsa_kv4_free). */
+RECSA_API recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t batch,
+                                      int32_t max_queries, void* cache, size_t cache_bytes,
+                                      void* workspace, size_t workspace_bytes, void* stream,
+                                      recsa_kv4** out);
+
+/* Set the length of sequence b to lengths[b] (host array, 0 <= lengths[b] <= capacity)
+ * and write rows 0 .. lengths[b] - 1 from k and v: element (b, h, t, :) at base +
+ * b*s[0] + h*s[1] + t*s[2] elements as in recsa_tree_init (so a tree's level-0 cache can
+ * be given as it is), 16-byte aligned, strides multiples of 16 bytes, s[2] >= d.  Every
+ * weight becomes 0, positions 0 .. lengths[b] - 1. */
+RECSA_API recsa_status recsa_kv4_build(recsa_kv4* kv4, const void* k, const void* v,
+                                       const int64_t kv_strides[3], const int64_t* lengths,
+                                       void* stream);
+
+/* Append tokens: k_new, v_new are device arrays [batch][Hkv][n][d] (contiguous, 16-byte
+ * aligned), n >= 1.  counts: optional device int32 [batch], 0 <= counts[b] <= n: only the
+ * first counts[b] rows of sequence b are appended (the rest is not read).  New rows have
+ * weight 0.  A sequence that would pass the capacity is left unchanged and the status
+ * word records RECSA_E_CAPACITY; a count out of range is taken as 0 and recorded as
+ * RECSA_E_DEVICE. */
+RECSA_API recsa_status recsa_kv4_append(recsa_kv4* kv4, const void* k_new, const void* v_new,
+                                        int32_t n, const int32_t* counts, void* stream);
+
+/* One query per sequence over all its cached tokens.  q, out: [batch][Hq][d] device,
+ * 16-byte aligned.  A sequence of length 0 gets zeros.  accumulate != 0: the weight of
+ * every slot (per KV head) also grows by the sum over the G query heads of its softmax
+ * probability. */
+RECSA_API recsa_status recsa_kv4_decode(recsa_kv4* kv4, const void* q, void* out,
+                                        int32_t accumulate, void* stream);
+
+/* Causal queries of the newest tokens, which are already appended.  Q, O:
+ * [batch][n][Hq][d] device.  Row i of sequence b sits at position P_b - n_b + i, where P_b
+ * is the number of tokens appended so far and n_b = counts[b] (n without counts), and sees
+ * the cached tokens up to that position.  Rows i >= n_b are neither read nor written.  A
+ * count out of range, or above P_b, is recorded as RECSA_E_DEVICE and its rows are skipped.
+ * A row that sees no token gets zeros.  accumulate_rows: the newest that many rows of each
+ * sequence add to the weights as recsa_kv4_decode does (0: none). */
+RECSA_API recsa_status recsa_kv4_prefill_chunk(recsa_kv4* kv4, const void* Q, int32_t n,
+                                               const int32_t* counts, void* O,
+                                               int32_t accumulate_rows, void* stream);
+
+/* Shrink every (sequence, KV head) that holds more than `budget` >= 1 tokens to `budget`:
+ * tokens at positions < n_first and the newest n_recent ones (positions >= P_b - n_recent)
+ * stay, and of the others those of the largest weights; ties stay in the order of their
+ * slots, a NaN weight ranks lowest.  n_first + n_recent <= budget.  Kept rows in slots >=
+ * budget move, with position and weight, into the slots < budget that became free: the
+ * j-th such row (by slot) into the j-th free slot.  Nothing else moves. */
+RECSA_API recsa_status recsa_kv4_evict(recsa_kv4* kv4, int64_t budget, int64_t n_first,
+                                       int64_t n_recent, void* stream);
+
+/* The values of slots start .. start + n - 1 (start + n <= capacity) in the storage dtype:
+ * k_out, v_out [batch][Hkv][n][d] device, 16-byte aligned, either may be NULL.  Slots at
+ * or past a sequence's length give zeros. */
+RECSA_API recsa_status recsa_kv4_read(recsa_kv4* kv4, int64_t start, int64_t n, void* k_out,
+                                      void* v_out, void* stream);
+
+/* Read and clear the status word as recsa_get_status does (synchronises `stream`). */
+RECSA_API recsa_status recsa_kv4_get_status(recsa_kv4* kv4, void* stream);
+
+/* Where things lie.  rows: rows per (sequence, KV head) of every table in the cache
+ * buffer (the capacity rounded up to a multiple of 128); row i of head h of sequence b is
+ * row (b*Hkv + h)*rows + i.  Offsets into the cache buffer: codes (d/2 bytes a row, dim 2j
+ * in the low nibble of byte j), params (d/32 words a row, s in the low half, lo in the
+ * high half, bf16), positions (int32) and weights (fp32; the caller may write weights of
+ * slots below the length).  Offsets into the workspace: lengths and tokens_seen (int64
+ * [batch], read only). */
+typedef struct {
+    int64_t capacity, rows;
+    int32_t batch, max_queries;
+    int64_t k_codes, v_codes, k_params, v_params, positions, weights;
+    int64_t lengths, tokens_seen;
+} recsa_kv4_info_t;
+RECSA_API recsa_status recsa_kv4_info(const recsa_kv4* kv4, recsa_kv4_info_t* info);
+
+/* Free the host handle.  Device memory stays with the caller. */
+RECSA_API recsa_status recsa_kv4_free(recsa_kv4* kv4);
+
 RECSA_API const char* recsa_status_str(recsa_status s);
 
 #ifdef __cplusplus

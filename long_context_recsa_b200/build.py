@@ -8,12 +8,14 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "librecsa.so")
 SOURCES = ["recsa_api.cu", "tree_kernels.cu", "select_attend.cu", "prefill_tc.cu", "noalloc.cu",
-           "gated.cu", "offload.cu"]
+           "gated.cu", "offload.cu", "kv4_api.cu", "kv4_rows.cu", "kv4_attend.cu",
+           "kv4_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -28,10 +30,19 @@ def nvcc_path() -> str:
 
 
 def _stale(out: str, deps) -> bool:
-    if not os.path.exists(out):
+    if deps is None or not os.path.exists(out):
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _compiled_from(depfile: str):
+    """The files that a make-style dependency file lists; None without one."""
+    if not os.path.exists(depfile):
+        return None
+    with open(depfile) as f:
+        names = f.read().replace("\\\n", " ").split(":", 1)[-1].split()
+    return names if all(os.path.exists(n) for n in names) else None
 
 
 OUT_BOUNDS = os.path.join(HERE, "librecsa_bounds.so")
@@ -47,15 +58,31 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     deps.append(os.path.join(HERE, "..", "include", "recsa.h"))
     if not force and not _stale(out, deps):
         return out
-    cmd = [nvcc_path(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared",
-           "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-o", out + ".tmp", *[os.path.join(CSRC, s) for s in SOURCES]]
+    # one object per source, compiled side by side; an object newer than every file it
+    # was compiled from (listed in its .d file) is kept
+    objdir = os.path.join(HERE, "_build", "bounds" if debug_bounds else "release")
+    os.makedirs(objdir, exist_ok=True)
+    flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
+             "-Xcompiler", "-fvisibility=hidden"]
     if debug_bounds:
-        cmd.insert(1, "-DRECSA_DEBUG_BOUNDS")
+        flags.append("-DRECSA_DEBUG_BOUNDS")
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+        flags.append("-Xptxas=-v")
+
+    def compile_one(src: str) -> str:
+        path = os.path.join(CSRC, src)
+        obj = os.path.join(objdir, src + ".o")
+        if force or _stale(obj, _compiled_from(obj + ".d")):
+            cmd = [nvcc_path(), *flags, "-MD", "-MF", obj + ".d", "-c", "-o", obj + ".tmp", path]
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            subprocess.run(cmd, check=True)
+            os.replace(obj + ".tmp", obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=max(1, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
+    subprocess.run([nvcc_path(), *ARCH, "-shared", "-o", out + ".tmp", *objs], check=True)
     os.replace(out + ".tmp", out)
     return out
 

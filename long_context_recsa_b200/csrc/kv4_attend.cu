@@ -1,0 +1,1001 @@
+// Attention over the 4-bit KV cache, for single tokens and for chunks:
+//
+//   o_r = sum_t p_rt V_t,   p_rt = exp(scale q_r . K_t) / sum_t' exp(scale q_r . K_t')
+//
+// with K_t, V_t = lo + s * code in groups of 32 dims (kv4.cuh), over the tokens that row
+// r may see.  Decode reads 160 bytes a token and KV head (d = 128) and computes 4 d G
+// flops on them, so it is bound by the cache read; dequantising every code to a float
+// would cost more issue slots than the bytes take to arrive, so no code is dequantised:
+//
+//   * A nibble in place in a 16-bit half is a subnormal fp16 number, code * 2^-24 (or
+//     code * 2^-20 for the nibble above it), exact.  `word & 0x000f000f` is therefore two
+//     operand elements of mma.sync.m16n8k16 (fp16 in, fp32 accumulators), and a word of
+//     eight codes costs four ANDs and one shift.
+//   * Scores: S[16 tokens x 8 columns] per group of 32 dims from two MMAs with the codes
+//     as A (ldmatrix of the packed rows) and q as B, then s and lo enter in fp32:
+//     S += s_tg * (code . q)_tg + lo_tg * (sum of q over g).
+//   * Output: O^T[32 dims x 8 columns] += codes^T P' with P' = p_rt * s_tg as B.
+//     ldmatrix.trans on 16-bit units (four codes) puts tokens 2t, 2t + 1 of four dims into
+//     one register, so the same masks give the A operands; p's accumulator layout becomes
+//     B's by one movmatrix.  Codes enter as code - 8: codes are never negative, so without
+//     that O would be a small difference of two large sums.  sum p (lo + 8 s) is kept in
+//     fp32 beside it.
+//
+// Precision.  q enters as fp16 scaled by a power of two to [2^10, 2^11): a bf16 q is exact
+// there.  P' enters as fp16, off by at most 2^-12 relative, less than bf16's own 2^-9 of
+// the output.  fp32 tensors use two fp16 columns a row for q and for P' (high and low
+// part, 22 bits; the low part of P' is scaled by 2^11, so that it keeps its bits where P'
+// itself is below fp16's normal range).  The softmax maximum, its sum and all accumulators are fp32.
+//
+// Work.  A unit is (sequence, KV head, block of 8 to 32 rows); its cache is cut into tiles
+// of 32 tokens.  All tiles of all units form one list, cut evenly over a persistent grid
+// (so ragged batches balance); a CTA's warps take its tiles in turn, each with its own ring
+// of TMA stages, running maximum and accumulators, and meet only at the end of a unit.  A
+// unit cut over several CTAs is joined by the last of them, in the order of the CTAs.
+#include <type_traits>
+
+#include "kv4.cuh"
+
+namespace recsa {
+
+namespace {
+
+constexpr int kTile = 32;            // tokens of a warp's stage
+constexpr int kAttendWarps = 4;
+constexpr int kAttendThreads = kAttendWarps * 32;
+constexpr int kStagesKv4 = 2;
+constexpr int kGridMax = 148 * 4;
+constexpr float kSlack = 6.0f;       // p may reach 2^6 before the running maximum moves
+constexpr float kLowUp = 2048.0f;    // fp32 tensors: scale of the low part of P' (its own column)
+
+template <int D>
+struct Stage {
+    static constexpr int kCodes = kTile * D / 2;
+    static constexpr int kPars = kTile * D / 8;
+    static constexpr int kK = 0, kV = kCodes, kKp = 2 * kCodes, kVp = 2 * kCodes + kPars;
+    static constexpr int kPos = 2 * kCodes + 2 * kPars;
+    // a multiple of the swizzle pattern (512 bytes for 64-byte rows, 256 for 32-byte)
+    static constexpr int kBytes = ((kPos + kTile * 4) + 511) / 512 * 512;
+};
+
+// Byte offset of 16-byte chunk `ch` (one group) of row r in a swizzled tile.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
+    if constexpr (D == 128) return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+    return (uint32_t)(r * 32 + ((ch ^ ((r >> 2) & 1)) << 4));
+}
+
+__device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* m, int row, int unit,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(0), "r"(row), "r"(unit), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+// Both halves minus 8 codes (low nibble: 8 * 2^-24; the nibble above it: 8 * 2^-20), exact.
+__device__ __forceinline__ uint32_t centre_lo(uint32_t x) {
+    __half2 a = *reinterpret_cast<__half2*>(&x);
+    const uint32_t m = 0x80088008u;
+    a = __hadd2(a, *reinterpret_cast<const __half2*>(&m));
+    return *reinterpret_cast<uint32_t*>(&a);
+}
+__device__ __forceinline__ uint32_t centre_hi(uint32_t x) {
+    __half2 a = *reinterpret_cast<__half2*>(&x);
+    const uint32_t m = 0x80808080u;
+    a = __hadd2(a, *reinterpret_cast<const __half2*>(&m));
+    return *reinterpret_cast<uint32_t*>(&a);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^e for a whole e, clamped to the normal range.
+__device__ __forceinline__ float pow2i(int e) {
+    e = e < -126 ? -126 : e > 127 ? 127 : e;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ int exponent_of(float x) {   // floor(log2 |x|), -127 for 0
+    return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
+}
+
+// Rows of a column set (8 MMA columns): one column a row, or a high and a low column.
+template <int T> constexpr int rows_of_set() { return 8 / T; }
+// Rows whose columns a lane holds in an accumulator.
+template <int T> constexpr int rows_of_lane() { return 2 / T; }
+
+// The block of rows a unit's MMA columns hold, staged once per unit in shared memory.
+template <int D, int T, int NCS>
+struct Rows {
+    static constexpr int NG = D / kKv4Group;
+    static constexpr int RB = NCS * 8 / T;
+    uint4 frag[NCS][NG][32];         // B operands of the two MMAs of a group, by lane
+    float sum[RB][NG];               // sums of q over a group, in the MMAs' scale
+    float scale[RB];                 // accumulator -> score in log2 units
+    int lim[RB];                     // last position the row sees, -1: no row
+};
+
+// Stages rows row0 .. row0 + RB - 1 of (b, h) (row = chunk row * G + head of the group).
+// One warp per row in turn; `n_b` rows of the sequence are in use, positions end at `seen`.
+template <int D, int T, int NCS>
+__device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query& qv, int b, int h,
+                           int row0, int row_end, int n_b, int64_t seen, int warp, int nwarps,
+                           int lane) {
+    constexpr int RB = NCS * 8 / T, E = D / 32;
+    using TI = typename std::conditional<T == 1, __nv_bfloat16, float>::type;
+    for (int r = warp; r < RB; r += nwarps) {
+        const int row = row0 + r, i = row / c.G, g = row % c.G;
+        const bool live = row < row_end && i < n_b;
+        float x[E];                  // dims lane * E ..: a group is 32 / E lanes
+        if (live) {
+            const TI* q = reinterpret_cast<const TI*>(qv.q) +
+                          (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = (float)q[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.0f;
+        }
+        float mx = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        const int e0 = exponent_of(mx), ex = e0 < -116 ? -116 : e0;
+        const float up = pow2i(10 - ex);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] *= up;
+            sum += x[e];
+        }
+        // the sum over the group's 32 / E lanes
+#pragma unroll
+        for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        if (lane % (32 / E) == 0) rs.sum[r][lane / (32 / E)] = sum * 0x1p-24f;
+        if (lane == 0) {
+            rs.scale[r] = fminf(c.scale * 1.4426950408889634f * pow2i(ex - 10) * 0x1p24f, 3e38f);
+            rs.lim[r] = live ? (int)(seen - n_b + i) : -1;
+        }
+        // dim 8t + k of a group (k < 8) sits in 16-bit unit (k >> 1 with the pairs
+        // (0,4), (1,5), (2,6), (3,7)) of lane (column, t); odd pairs meet codes * 16
+        __half* f = reinterpret_cast<__half*>(&rs.frag[r / (8 / T)][0][0]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int dim = lane * E + e, grp = dim / 32, t = (dim / 8) & 3, k = dim & 7;
+            const float y = (k & 1) ? x[e] * 0.0625f : x[e];
+            const int reg = k & 3, half = k >> 2;
+            if constexpr (T == 1) {
+                const int l = (r & 7) * 4 + t;
+                f[((grp * 32 + l) * 4 + reg) * 2 + half] = __float2half_rn(y);
+            } else {
+                const int l = (r & 3) * 2 * 4 + t;
+                const __half hi = __float2half_rn(y);
+                f[((grp * 32 + l) * 4 + reg) * 2 + half] = hi;
+                f[((grp * 32 + l + 4) * 4 + reg) * 2 + half] = __float2half_rn(y - __half2float(hi));
+            }
+        }
+    }
+}
+
+template <int NG>
+__device__ __forceinline__ void load_pars(uint32_t (&p)[NG], const unsigned char* base, int row) {
+    if constexpr (NG == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(base + row * 16);
+        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(base + row * 8);
+        p[0] = v.x; p[1] = v.y;
+    }
+}
+
+// Scores of 16 tokens (rows r0 .. r0 + 15 of a tile at `kc`) against every column set, in
+// the rows' scale: sc[c][2 * e + k] for the lane's row e and token g (k = 0) or g + 8.
+template <int D, int T, int NCS>
+__device__ __forceinline__ void scores16(float (&sc)[NCS][2 * (2 / T)], uint32_t kc,
+                                         const uint32_t (&p0)[D / 32], const uint32_t (&p1)[D / 32],
+                                         const Rows<D, T, NCS>& rs,
+                                         const uint4 (&qreg)[NCS == 1 ? D / 32 : 1],
+                                         const float (&qsum)[NCS == 1 ? 2 / T : 1][D / 32],
+                                         int r0, int lane) {
+    constexpr int NG = D / kKv4Group, RL = 2 / T;
+    const int t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < NCS; ++c)
+#pragma unroll
+        for (int e = 0; e < 2 * RL; ++e) sc[c][e] = 0.0f;
+#pragma unroll
+    for (int j2 = 0; j2 < NG; j2 += 2) {
+        uint32_t w[4];   // tokens 0-7 and 8-15 of group j2, then of j2 + 1
+        ldsm4(w, kc + chunk_at<D>(r0 + (lane & 15), j2 + (lane >> 4)));
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            const int j = j2 + jj;
+            const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
+            uint32_t a[8] = {wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
+                             (wa >> 8) & 0x000f000fu, (wb >> 8) & 0x000f000fu,
+                             (wa >> 8) & 0x00f000f0u, (wb >> 8) & 0x00f000f0u};
+            float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
+            float o0 = kv4_off(p0[j]), o1 = kv4_off(p1[j]);
+            if constexpr (T == 2) {
+                // fp32: centred codes, so that the two terms of a score stay small
+                a[0] = centre_lo(a[0]); a[1] = centre_lo(a[1]);
+                a[2] = centre_hi(a[2]); a[3] = centre_hi(a[3]);
+                a[4] = centre_lo(a[4]); a[5] = centre_lo(a[5]);
+                a[6] = centre_hi(a[6]); a[7] = centre_hi(a[7]);
+                o0 = fmaf(8.0f, s0, o0);
+                o1 = fmaf(8.0f, s1, o1);
+            }
+#pragma unroll
+            for (int c = 0; c < NCS; ++c) {
+                uint4 q;
+                if constexpr (NCS == 1) q = qreg[j]; else q = rs.frag[c][j][lane];
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(acc, a[0], a[1], a[2], a[3], q.x, q.y);
+                mma16816(acc, a[4], a[5], a[6], a[7], q.z, q.w);
+                if constexpr (T == 1) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float qs = NCS == 1 ? qsum[e][j] : rs.sum[c * 8 + 2 * t + e][j];
+                        sc[c][2 * e] = fmaf(s0, acc[e], fmaf(o0, qs, sc[c][2 * e]));
+                        sc[c][2 * e + 1] = fmaf(s1, acc[2 + e], fmaf(o1, qs, sc[c][2 * e + 1]));
+                    }
+                } else {
+                    const float qs = NCS == 1 ? qsum[0][j] : rs.sum[c * 4 + t][j];
+                    sc[c][0] = fmaf(s0, acc[0] + acc[1], fmaf(o0, qs, sc[c][0]));
+                    sc[c][1] = fmaf(s1, acc[2] + acc[3], fmaf(o1, qs, sc[c][1]));
+                }
+            }
+        }
+    }
+}
+
+// The warps' stages; at the end of a unit their partial outputs lie over them.
+template <int D, int RB>
+__host__ __device__ constexpr size_t ring_bytes() {
+    const size_t stages = (size_t)kAttendWarps * kStagesKv4 * Stage<D>::kBytes;
+    const size_t partials = (size_t)kAttendWarps * RB * D * sizeof(float);
+    return stages > partials ? stages : partials;
+}
+// CTAs an SM holds: 128 registers a thread carry one column set, 255 four.
+template <int NCS> constexpr int ctas_per_sm() { return NCS == 1 ? 4 : NCS == 2 ? 3 : 2; }
+
+// The tiles of a launch: sequence b has nrb[b] blocks of rows a KV head, each over
+// tiles[b] tiles of its cache; `pre` are their running totals over b.
+struct Plan {
+    int64_t pre[RECSA_MAX_BATCH + 1];
+    int tiles[RECSA_MAX_BATCH];
+    int nrb[RECSA_MAX_BATCH];
+};
+
+__device__ __forceinline__ void make_plan(Plan& pl, const Kv4View& c, const Kv4Query& qv, int RB,
+                                          bool one_block, bool chunk, int lane) {
+    // warp 0: two sequences a lane
+    int64_t v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int b = 2 * lane + k;
+        v[k] = 0;
+        if (b < c.B) {
+            const int64_t L = c.len[b];
+            int n_b = (int)kv4_count(qv.counts, b, qv.n, c.status);
+            if (chunk && n_b > c.seen[b]) {   // more rows than tokens: none has a position
+                set_status(c.status, kStatusBadQuery);
+                n_b = 0;
+            }
+            int rows = n_b - qv.i0;
+            rows = rows < 0 ? 0 : rows < qv.w ? rows : qv.w;
+            const int nrb = one_block ? (rows > 0 ? 1 : 0) : (rows * c.G + RB - 1) / RB;
+            // a block whose sequence is empty still has its zero rows to write
+            const int tiles = (int)((L + kTile - 1) / kTile) + (L == 0 ? 1 : 0);
+            pl.tiles[b] = tiles;
+            pl.nrb[b] = nrb;
+            v[k] = (int64_t)c.Hkv * nrb * tiles;
+        }
+    }
+    int64_t x = v[0] + v[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+    }
+    const int64_t before = x - v[0] - v[1];
+    if (2 * lane < c.B) pl.pre[2 * lane] = before;
+    if (2 * lane + 1 < c.B) pl.pre[2 * lane + 1] = before + v[0];
+    const int64_t total = __shfl_sync(kFull, x, 31);
+    if (lane == 0) pl.pre[c.B] = total;
+}
+
+}  // namespace
+
+template <int D, int T, int NCS, bool CHUNK>
+__global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend_kernel(
+    Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps) {
+    constexpr int NG = D / kKv4Group, RB = NCS * 8 / T, RL = 2 / T, RS = 8 / T;
+    using St = Stage<D>;
+    using RowsT = Rows<D, T, NCS>;
+    using TI = typename std::conditional<T == 1, __nv_bfloat16, float>::type;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* ring = smem;
+    RowsT& rs = *reinterpret_cast<RowsT*>(smem + ring_bytes<D, RB>());
+    __shared__ Plan pl;
+    __shared__ uint64_t bars[kAttendWarps][kStagesKv4];
+    __shared__ float red_m[kAttendWarps][RB], red_l[kAttendWarps][RB];
+    __shared__ int last_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kAttendWarps; ++w)
+            for (int s = 0; s < kStagesKv4; ++s) mbar_init(&bars[w][s], 1);
+        mbar_fence_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 0) make_plan(pl, c, qv, RB, false, CHUNK, lane);
+    __syncthreads();
+    const int64_t total = pl.pre[c.B];
+    int64_t quota = (total + gridDim.x - 1) / gridDim.x;
+    if (quota < kAttendWarps) quota = kAttendWarps;   // one tile a warp at least
+    int64_t at = blockIdx.x * quota;
+    int64_t at_end = at + quota < total ? at + quota : total;
+    uint32_t phase = 0;                                // bit s: parity of stage s
+    bool alive = true;                                 // no wait of this warp gave up
+    unsigned char* my_ring = ring + warp * kStagesKv4 * St::kBytes;
+
+    int b = 0;
+    while (at < at_end) {
+        while (pl.pre[b + 1] <= at) ++b;
+        const int tiles = pl.tiles[b], nrb = pl.nrb[b];
+        const int64_t in_b = at - pl.pre[b];
+        const int64_t uu = in_b / tiles;               // (h, block) of sequence b
+        const int tile0 = (int)(in_b - uu * tiles);
+        const int tile1 = (int)(at_end - at < tiles - tile0 ? at_end - at + tile0 : tiles);
+        const int h = (int)(uu / nrb), rb = (int)(uu % nrb);
+        const int u = b * c.Hkv + h;
+        const int64_t L = c.len[b];
+        const int n_b = qv.counts ? qv.counts[b] : qv.n;
+        const int row0 = qv.i0 * c.G + rb * RB;
+        const int w_end = qv.i0 + qv.w < n_b ? qv.i0 + qv.w : n_b;
+        const int row_end = w_end * c.G;
+
+        auto fetch = [&](int tile, int s) {
+            unsigned char* st = my_ring + s * St::kBytes;
+            uint64_t* bar = &bars[warp][s];
+            const int64_t r = (int64_t)tile * kTile;
+            mbar_expect_tx(bar, 2 * St::kCodes + 2 * St::kPars + (CHUNK ? kTile * 4 : 0));
+            tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
+            tma_rows(st + St::kV, &maps.v, (int)r, u, bar);
+            bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
+            bulk_g2s(st + St::kVp, c.vp + (u * c.R + r) * NG, St::kPars, bar);
+            if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
+        };
+        const int mine = L > 0 ? (tile1 - tile0 - warp + kAttendWarps - 1) / kAttendWarps : 0;
+        if (lane == 0 && alive)
+            for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + warp + s * kAttendWarps, s);
+        stage_rows<D, T, NCS>(rs, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp, kAttendWarps, lane);
+        __syncthreads();
+
+        // V's steps enter P' scaled so that the unit's largest is at most 2^8
+        // (s <= 2.02 vmax / 15 < 2^ev), so P' stays below 2^14
+        const int e0 = exponent_of(__uint_as_float(c.vmax[u])) - 1, ev = e0 < -118 ? -118 : e0;
+        const float vf = pow2i(8 - ev);
+        const float vinv = pow2i(ev - 8);
+
+        float O[NCS][NG][2][4], bias[NCS][RL][NG], m[NCS][RL], l[NCS][RL], rsc[NCS][RL];
+        int lim[NCS][RL];
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[cs][j][k][e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < RL; ++e) {
+                m[cs][e] = kKv4MinLog2;
+                l[cs][e] = 0.0f;
+                rsc[cs][e] = rs.scale[cs * RS + t * RL + e];
+                lim[cs][e] = rs.lim[cs * RS + t * RL + e];
+#pragma unroll
+                for (int j = 0; j < NG; ++j) bias[cs][e][j] = 0.0f;
+            }
+        }
+        uint4 qreg[NCS == 1 ? NG : 1];
+        float qsum[NCS == 1 ? RL : 1][NG];
+        if constexpr (NCS == 1) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                qreg[j] = rs.frag[0][j][lane];
+#pragma unroll
+                for (int e = 0; e < RL; ++e) qsum[e][j] = rs.sum[t * RL + e][j];
+            }
+        }
+
+        for (int it = 0; it < mine; ++it) {
+            const int s = it % kStagesKv4;
+            const int tile = tile0 + warp + it * kAttendWarps;
+            if (!alive) break;
+            if (!__all_sync(kFull, mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status))) {
+                alive = false;
+                break;
+            }
+            phase ^= 1u << s;
+            const unsigned char* st = my_ring + s * St::kBytes;
+            const uint32_t sa = smem_u32(st);
+            const bool tail = (int64_t)(tile + 1) * kTile > L;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int r0 = half * 16;
+                const int64_t tok = (int64_t)tile * kTile + r0 + g;
+                if (tail && tok - g >= L) break;       // nothing in this half (uniform)
+                uint32_t p0[NG], p1[NG];
+                load_pars<NG>(p0, st + St::kKp, r0 + g);
+                load_pars<NG>(p1, st + St::kKp, r0 + g + 8);
+                float sc[NCS][2 * RL];
+                scores16<D, T, NCS>(sc, sa + St::kK, p0, p1, rs, qreg, qsum, r0, lane);
+                load_pars<NG>(p0, st + St::kVp, r0 + g);
+                load_pars<NG>(p1, st + St::kVp, r0 + g + 8);
+                int pos0 = -1, pos1 = -1;
+                if (CHUNK) {
+                    pos0 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g) * 4);
+                    pos1 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g + 8) * 4);
+                }
+                if (tail) {
+                    // rows past the length: whatever they hold must not enter a product
+                    if (tok >= L) {
+                        pos0 = 0x7fffffff;
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) p0[j] = 0;
+                    }
+                    if (tok + 8 >= L) {
+                        pos1 = 0x7fffffff;
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) p1[j] = 0;
+                    }
+                }
+                bool grow = false;
+#pragma unroll
+                for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                    for (int e = 0; e < RL; ++e) {
+                        sc[cs][2 * e] *= rsc[cs][e];
+                        sc[cs][2 * e + 1] *= rsc[cs][e];
+                        if (CHUNK || tail) {
+                            const int lm = CHUNK ? lim[cs][e] : 0x7ffffffe;
+                            if (pos0 > lm) sc[cs][2 * e] = -INFINITY;
+                            if (pos1 > lm) sc[cs][2 * e + 1] = -INFINITY;
+                        }
+                        grow |= fmaxf(sc[cs][2 * e], sc[cs][2 * e + 1]) > m[cs][e] + kSlack;
+                    }
+                if (__any_sync(kFull, grow)) {
+#pragma unroll
+                    for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                        for (int e = 0; e < RL; ++e) {
+                            float x = fmaxf(sc[cs][2 * e], sc[cs][2 * e + 1]);
+                            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                            const float mn = fmaxf(m[cs][e], x);
+                            const float f = ex2(m[cs][e] - mn);
+                            m[cs][e] = mn;
+                            l[cs][e] *= f;
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) {
+                                bias[cs][e][j] *= f;
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    if constexpr (T == 1) {
+                                        O[cs][j][k][e] *= f;
+                                        O[cs][j][k][2 + e] *= f;
+                                    } else {
+#pragma unroll
+                                        for (int z = 0; z < 4; ++z) O[cs][j][k][z] *= f;
+                                    }
+                                }
+                            }
+                        }
+                }
+#pragma unroll
+                for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                    for (int e = 0; e < RL; ++e) {
+                        sc[cs][2 * e] = ex2(sc[cs][2 * e] - m[cs][e]);
+                        sc[cs][2 * e + 1] = ex2(sc[cs][2 * e + 1] - m[cs][e]);
+                        l[cs][e] += sc[cs][2 * e] + sc[cs][2 * e + 1];
+                    }
+                uint32_t nan0 = 0, nan1 = 0;
+#pragma unroll
+                for (int j2 = 0; j2 < NG; j2 += 2) {
+                    uint32_t w[4];
+                    ldsm4t(w, sa + St::kV + chunk_at<D>(r0 + (lane & 15), j2 + (lane >> 4)));
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        const int j = j2 + jj;
+                        const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
+                        // dims 4g + k of the group, tokens 2t, 2t + 1 (wa) and + 8 (wb)
+                        const uint32_t a0 = centre_lo(wa & 0x000f000fu);
+                        const uint32_t a1 = centre_hi(wa & 0x00f000f0u);
+                        const uint32_t a2 = centre_lo(wb & 0x000f000fu);
+                        const uint32_t a3 = centre_hi(wb & 0x00f000f0u);
+                        const uint32_t a4 = centre_lo((wa >> 8) & 0x000f000fu);
+                        const uint32_t a5 = centre_hi((wa >> 8) & 0x00f000f0u);
+                        const uint32_t a6 = centre_lo((wb >> 8) & 0x000f000fu);
+                        const uint32_t a7 = centre_hi((wb >> 8) & 0x00f000f0u);
+                        const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
+                        float c0 = fmaf(8.0f, s0, kv4_off(p0[j]));
+                        float c1 = fmaf(8.0f, s1, kv4_off(p1[j]));
+                        if (CHUNK) {
+                            // a NaN group must not reach rows that do not see its token
+                            if (c0 != c0) { c0 = 0.0f; nan0 |= 1u << j; }
+                            if (c1 != c1) { c1 = 0.0f; nan1 |= 1u << j; }
+                        }
+                        const float f0 = s0 * vf, f1 = s1 * vf;
+#pragma unroll
+                        for (int cs = 0; cs < NCS; ++cs) {
+                            uint32_t b0, b1;
+                            if constexpr (T == 1) {
+                                b0 = movm(pack_h2(sc[cs][0] * f0, sc[cs][2] * f0));
+                                b1 = movm(pack_h2(sc[cs][1] * f1, sc[cs][3] * f1));
+                            } else {
+                                const float x0 = sc[cs][0] * f0, x1 = sc[cs][1] * f1;
+                                const float h0 = __half2float(__float2half_rn(x0));
+                                const float h1 = __half2float(__float2half_rn(x1));
+                                b0 = movm(pack_h2(h0, (x0 - h0) * kLowUp));
+                                b1 = movm(pack_h2(h1, (x1 - h1) * kLowUp));
+                            }
+#pragma unroll
+                            for (int e = 0; e < RL; ++e)
+                                bias[cs][e][j] = fmaf(sc[cs][2 * e], c0,
+                                                      fmaf(sc[cs][2 * e + 1], c1, bias[cs][e][j]));
+                            mma16816(O[cs][j][0], a0, a1, a2, a3, b0, b1);
+                            mma16816(O[cs][j][1], a4, a5, a6, a7, b0, b1);
+                        }
+                    }
+                }
+                if (CHUNK && (nan0 | nan1)) {
+#pragma unroll
+                    for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                        for (int e = 0; e < RL; ++e)
+#pragma unroll
+                            for (int j = 0; j < NG; ++j)
+                                if ((((nan0 >> j) & 1u) && pos0 <= lim[cs][e]) ||
+                                    (((nan1 >> j) & 1u) && pos1 <= lim[cs][e]))
+                                    bias[cs][e][j] = NAN;
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && it + kStagesKv4 < mine)
+                fetch(tile0 + warp + (it + kStagesKv4) * kAttendWarps, s);
+        }
+        if (!alive) {
+            // a copy never came: let what is in flight land before the stages are reused
+            for (int s = 0; s < kStagesKv4; ++s)
+                if (lane == 0) mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status, kWaitPollsAfterFail);
+        }
+
+        // ---- the warps' results of the unit meet in shared memory (over the ring) ----
+        __syncthreads();
+        float* red = reinterpret_cast<float*>(ring);   // [warp][RB][D]
+#pragma unroll
+        for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+            for (int e = 0; e < RL; ++e) {
+                const int r = cs * RS + t * RL + e;
+                float ls = l[cs][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) ls += __shfl_xor_sync(kFull, ls, o);
+                if (g == 0) {
+                    red_m[warp][r] = m[cs][e];
+                    red_l[warp][r] = ls;
+                }
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    float bs = bias[cs][e][j];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) bs += __shfl_xor_sync(kFull, bs, o);
+                    float4 v;
+                    if constexpr (T == 1) {
+                        v.x = O[cs][j][0][e];
+                        v.y = O[cs][j][0][2 + e] * 0.0625f;
+                        v.z = O[cs][j][1][e];
+                        v.w = O[cs][j][1][2 + e] * 0.0625f;
+                    } else {
+                        v.x = fmaf(O[cs][j][0][1], 1.0f / kLowUp, O[cs][j][0][0]);
+                        v.y = fmaf(O[cs][j][0][3], 1.0f / kLowUp, O[cs][j][0][2]) * 0.0625f;
+                        v.z = fmaf(O[cs][j][1][1], 1.0f / kLowUp, O[cs][j][1][0]);
+                        v.w = fmaf(O[cs][j][1][3], 1.0f / kLowUp, O[cs][j][1][2]) * 0.0625f;
+                    }
+                    v.x = fmaf(v.x * 0x1p24f, vinv, bs);
+                    v.y = fmaf(v.y * 0x1p24f, vinv, bs);
+                    v.z = fmaf(v.z * 0x1p24f, vinv, bs);
+                    v.w = fmaf(v.w * 0x1p24f, vinv, bs);
+                    *reinterpret_cast<float4*>(red + ((size_t)warp * RB + r) * D + j * 32 + g * 4) = v;
+                }
+            }
+        __syncthreads();
+        const int64_t unit0 = at - tile0;              // first tile of the unit in the list
+        const int64_t cta0 = unit0 / quota, cta1 = (unit0 + tiles - 1) / quota;
+        const bool whole = cta0 == cta1;
+        auto store_row = [&](int r, int d4, float4 v, float mx, float ls) {
+            const int row = row0 + r;
+            if (row >= row_end) return;
+            const float inv = ls > 0.0f || ls != ls ? 1.0f / ls : 0.0f;
+            const int i = row / c.G, gg = row % c.G;
+            TI* o = reinterpret_cast<TI*>(qv.out) +
+                    (((int64_t)b * qv.n + i) * c.Hq + h * c.G + gg) * D + d4 * 4;
+            if constexpr (T == 2) {
+                *reinterpret_cast<float4*>(o) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            } else {
+                __nv_bfloat162 y[2] = {__floats2bfloat162_rn(v.x * inv, v.y * inv),
+                                       __floats2bfloat162_rn(v.z * inv, v.w * inv)};
+                *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(y);
+            }
+            if (d4 == 0 && sc_.lse)
+                sc_.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] =
+                    ls > 0.0f || ls != ls ? mx + log2f(ls) : INFINITY;
+        };
+        float* part = whole ? nullptr
+                            : sc_.part + (size_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * RB * (D + 2);
+        for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
+            const int r = i / (D / 4), d4 = i % (D / 4);
+            float mx = red_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kAttendWarps; ++w) mx = fmaxf(mx, red_m[w][r]);
+            float ls = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; ++w) {
+                const float f = ex2(red_m[w][r] - mx);
+                const float4 x = *reinterpret_cast<const float4*>(red + ((size_t)w * RB + r) * D + d4 * 4);
+                ls = fmaf(f, red_l[w][r], ls);
+                v.x = fmaf(f, x.x, v.x);
+                v.y = fmaf(f, x.y, v.y);
+                v.z = fmaf(f, x.z, v.z);
+                v.w = fmaf(f, x.w, v.w);
+            }
+            if (whole) {
+                store_row(r, d4, v, mx, ls);
+            } else {
+                *reinterpret_cast<float4*>(part + r * D + d4 * 4) = v;
+                if (d4 == 0) {
+                    part[RB * D + r] = mx;
+                    part[RB * D + RB + r] = ls;
+                }
+            }
+        }
+        if (!whole) {
+            // the last CTA of the unit joins the partials in the order of the CTAs
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                last_flag = atomicAdd(&sc_.ucnt[cta0], 1u) == (uint32_t)(cta1 - cta0);
+                if (last_flag) sc_.ucnt[cta0] = 0;
+            }
+            __syncthreads();
+            if (last_flag) {
+                __threadfence();
+                auto slot = [&](int64_t cta) {
+                    return sc_.part + (size_t)(2 * cta + (cta == cta0 ? 1 : 0)) * RB * (D + 2);
+                };
+                for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
+                    const int r = i / (D / 4), d4 = i % (D / 4);
+                    float mx = kKv4MinLog2;
+                    for (int64_t k = cta0; k <= cta1; ++k) mx = fmaxf(mx, __ldcg(slot(k) + RB * D + r));
+                    float ls = 0.0f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int64_t k = cta0; k <= cta1; ++k) {
+                        const float* p = slot(k);
+                        const float f = ex2(__ldcg(p + RB * D + r) - mx);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d4 * 4));
+                        ls = fmaf(f, __ldcg(p + RB * D + RB + r), ls);
+                        v.x = fmaf(f, x.x, v.x);
+                        v.y = fmaf(f, x.y, v.y);
+                        v.z = fmaf(f, x.z, v.z);
+                        v.w = fmaf(f, x.w, v.w);
+                    }
+                    store_row(r, d4, v, mx, ls);
+                }
+            }
+        }
+        at += tile1 - tile0;
+        // the next unit's copies overwrite what was just read and written here
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+    }
+}
+
+// Accumulated weights: w[slot] += sum over the newest acc_rows rows of every sequence
+// (all G heads) of exp2(score - lse), with the scores formed again from the keys as above
+// and the rows' lse from the attention launch before it.  Rows rb0 * RB .. of the rows
+// that count, up to NP blocks a launch, are held in shared memory; a tile's codes are
+// read once for all of them.  Every slot belongs to one warp, so sums have one order.
+template <int D, int T, bool CHUNK>
+__global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
+    Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,
+    int n_blocks) {
+    constexpr int NG = D / kKv4Group, RB = 8 / T, RL = 2 / T;
+    using St = Stage<D>;
+    using RowsT = Rows<D, T, 1>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* ring = smem;
+    RowsT* rs = reinterpret_cast<RowsT*>(smem + kAttendWarps * kStagesKv4 * St::kBytes);
+    float* lse = reinterpret_cast<float*>(rs + n_blocks);   // [n_blocks][RB]
+    __shared__ Plan pl;
+    __shared__ uint64_t bars[kAttendWarps][kStagesKv4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kAttendWarps; ++w)
+            for (int s = 0; s < kStagesKv4; ++s) mbar_init(&bars[w][s], 1);
+        mbar_fence_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 0) make_plan(pl, c, qv, RB, true, CHUNK, lane);
+    __syncthreads();
+    const int64_t total = pl.pre[c.B];
+    int64_t quota = (total + gridDim.x - 1) / gridDim.x;
+    if (quota < kAttendWarps) quota = kAttendWarps;
+    int64_t at = blockIdx.x * quota;
+    const int64_t at_end = at + quota < total ? at + quota : total;
+    uint32_t phase = 0;
+    bool alive = true;
+    unsigned char* my_ring = ring + warp * kStagesKv4 * St::kBytes;
+    int b = 0;
+    while (at < at_end) {
+        while (pl.pre[b + 1] <= at) ++b;
+        const int tiles = pl.tiles[b];
+        const int64_t in_b = at - pl.pre[b];
+        const int h = (int)(in_b / tiles);
+        const int tile0 = (int)(in_b - (int64_t)h * tiles);
+        const int tile1 = (int)(at_end - at < tiles - tile0 ? at_end - at + tile0 : tiles);
+        const int u = b * c.Hkv + h;
+        const int64_t L = c.len[b];
+        const int n_b = qv.counts ? qv.counts[b] : qv.n;
+        // the rows that count: the newest acc_rows of the sequence, within this wave
+        int i_lo = n_b - qv.acc_rows > qv.i0 ? n_b - qv.acc_rows : qv.i0;
+        const int i_hi = qv.i0 + qv.w < n_b ? qv.i0 + qv.w : n_b;
+        const int row0 = i_lo * c.G + first_row;
+        const int row_end = i_hi * c.G;
+        auto fetch = [&](int tile, int s) {
+            unsigned char* st = my_ring + s * St::kBytes;
+            uint64_t* bar = &bars[warp][s];
+            const int64_t r = (int64_t)tile * kTile;
+            mbar_expect_tx(bar, St::kCodes + St::kPars + (CHUNK ? kTile * 4 : 0));
+            tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
+            bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
+            if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
+        };
+        int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - warp + kAttendWarps - 1) / kAttendWarps : 0;
+        if (lane == 0 && alive)
+            for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + warp + s * kAttendWarps, s);
+        if (row0 < row_end) {
+            for (int k = 0; k < n_blocks; ++k) {
+                stage_rows<D, T, 1>(rs[k], c, qv, b, h, row0 + k * RB, row_end, n_b, c.seen[b], warp,
+                                    kAttendWarps, lane);
+                const int i = threadIdx.x;
+                if (i < RB) {
+                    const int row = row0 + k * RB + i;
+                    lse[k * RB + i] = row < row_end
+                        ? sc_.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] : INFINITY;
+                }
+            }
+        }
+        __syncthreads();
+        for (int it = 0; it < mine; ++it) {
+            const int s = it % kStagesKv4;
+            const int tile = tile0 + warp + it * kAttendWarps;
+            if (!alive) break;
+            if (!__all_sync(kFull, mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status))) {
+                alive = false;
+                break;
+            }
+            phase ^= 1u << s;
+            const unsigned char* st = my_ring + s * St::kBytes;
+            const uint32_t sa = smem_u32(st);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int r0 = half * 16;
+                const int64_t tok = (int64_t)tile * kTile + r0 + g;
+                if (tok - g >= L) break;
+                uint32_t p0[NG], p1[NG];
+                load_pars<NG>(p0, st + St::kKp, r0 + g);
+                load_pars<NG>(p1, st + St::kKp, r0 + g + 8);
+                int pos0 = -1, pos1 = -1;
+                if (CHUNK) {
+                    pos0 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g) * 4);
+                    pos1 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g + 8) * 4);
+                }
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 1
+                for (int k = 0; k < n_blocks; ++k) {
+                    if (row0 + k * RB >= row_end) break;
+                    uint4 qreg[NG];
+                    float qsum[RL][NG];
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        qreg[j] = rs[k].frag[0][j][lane];
+#pragma unroll
+                        for (int e = 0; e < RL; ++e) qsum[e][j] = rs[k].sum[t * RL + e][j];
+                    }
+                    float sc[1][2 * RL];
+                    scores16<D, T, 1>(sc, sa + St::kK, p0, p1, rs[k], qreg, qsum, r0, lane);
+#pragma unroll
+                    for (int e = 0; e < RL; ++e) {
+                        const float f = rs[k].scale[t * RL + e], ls = lse[k * RB + t * RL + e];
+                        const int lm = rs[k].lim[t * RL + e];
+                        const float x0 = ex2(sc[0][2 * e] * f - ls), x1 = ex2(sc[0][2 * e + 1] * f - ls);
+                        // rows that are not there have lm = -1, below every position
+                        if ((CHUNK ? pos0 : 0) <= lm) sum0 += x0;
+                        if ((CHUNK ? pos1 : 0) <= lm) sum1 += x1;
+                    }
+                }
+                sum0 += __shfl_xor_sync(kFull, sum0, 1);
+                sum1 += __shfl_xor_sync(kFull, sum1, 1);
+                sum0 += __shfl_xor_sync(kFull, sum0, 2);
+                sum1 += __shfl_xor_sync(kFull, sum1, 2);
+                if (t == 0) {
+                    float* w = c.w + u * c.R + tok;
+                    if (tok < L) w[0] += sum0;
+                    if (tok + 8 < L) w[8] += sum1;
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && it + kStagesKv4 < mine)
+                fetch(tile0 + warp + (it + kStagesKv4) * kAttendWarps, s);
+        }
+        if (!alive) {
+            for (int s = 0; s < kStagesKv4; ++s)
+                if (lane == 0) mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status, kWaitPollsAfterFail);
+        }
+        at += tile1 - tile0;
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------------
+namespace {
+
+template <int D, int T, int NCS>
+constexpr size_t attend_smem() {
+    return 1024 + ring_bytes<D, NCS * 8 / T>() + sizeof(Rows<D, T, NCS>);
+}
+template <int D, int T>
+constexpr size_t weights_smem(int blocks) {
+    return 1024 + (size_t)kAttendWarps * kStagesKv4 * Stage<D>::kBytes +
+           (size_t)blocks * (sizeof(Rows<D, T, 1>) + sizeof(float) * 8 / T);
+}
+constexpr int kWeightBlocks = 16;    // column sets a weights launch holds
+
+// Column sets of a block: the fewest that hold the rows, up to four (the accumulators of
+// four fill the register file).
+int sets_for(int T, int rows) {
+    const int per = 8 / T;
+    return rows <= per ? 1 : rows <= 2 * per ? 2 : 4;
+}
+
+template <typename K>
+cudaError_t allow(K kern, size_t smem) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+template <int D, int T>
+cudaError_t prepare_impl() {
+    cudaError_t e = allow(kv4_attend_kernel<D, T, 1, false>, attend_smem<D, T, 1>());
+    if constexpr (T == 2)
+        if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, false>, attend_smem<D, T, 2>());
+    if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 1, true>, attend_smem<D, T, 1>());
+    if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, true>, attend_smem<D, T, 2>());
+    if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 4, true>, attend_smem<D, T, 4>());
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false>, weights_smem<D, T>(kWeightBlocks));
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true>, weights_smem<D, T>(kWeightBlocks));
+    return e;
+}
+
+template <int D, int T>
+cudaError_t attend_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
+                        const Kv4Maps& maps, int chunk, cudaStream_t s) {
+    const int sets = sets_for(T, qv.w * c.G);
+    const dim3 grid(148 * (sets == 1 ? ctas_per_sm<1>() : sets == 2 ? ctas_per_sm<2>()
+                                                                     : ctas_per_sm<4>()));
+    if (!chunk) {
+        if (sets == 1)
+            return kv4_launch(kv4_attend_kernel<D, T, 1, false>, grid, kAttendThreads,
+                              attend_smem<D, T, 1>(), s, c, qv, sc, maps);
+        if constexpr (T == 2)
+            return kv4_launch(kv4_attend_kernel<D, T, 2, false>, grid, kAttendThreads,
+                              attend_smem<D, T, 2>(), s, c, qv, sc, maps);
+        return cudaErrorInvalidValue;   // bf16: 8 columns hold the 8 heads of the largest group
+    }
+    if (sets == 1)
+        return kv4_launch(kv4_attend_kernel<D, T, 1, true>, grid, kAttendThreads,
+                          attend_smem<D, T, 1>(), s, c, qv, sc, maps);
+    if (sets == 2)
+        return kv4_launch(kv4_attend_kernel<D, T, 2, true>, grid, kAttendThreads,
+                          attend_smem<D, T, 2>(), s, c, qv, sc, maps);
+    return kv4_launch(kv4_attend_kernel<D, T, 4, true>, grid, kAttendThreads,
+                      attend_smem<D, T, 4>(), s, c, qv, sc, maps);
+}
+
+template <int D, int T>
+cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
+                         const Kv4Maps& maps, int chunk, cudaStream_t s) {
+    const int rows = (qv.acc_rows < qv.w ? qv.acc_rows : qv.w) * c.G, per = 8 / T;
+    for (int r = 0; r < rows; r += kWeightBlocks * per) {
+        int blocks = (rows - r + per - 1) / per;
+        if (blocks > kWeightBlocks) blocks = kWeightBlocks;
+        const cudaError_t e =
+            chunk ? kv4_launch(kv4_weights_kernel<D, T, true>, dim3(kGridMax), kAttendThreads,
+                               weights_smem<D, T>(blocks), s, c, qv, sc, maps, r, blocks)
+                  : kv4_launch(kv4_weights_kernel<D, T, false>, dim3(kGridMax), kAttendThreads,
+                               weights_smem<D, T>(blocks), s, c, qv, sc, maps, r, blocks);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+int kv4_attend_grid() { return kGridMax; }
+size_t kv4_attend_part_floats(int D) { return (size_t)2 * kGridMax * 32 * (D + 2); }
+
+#define KV4_ATTEND(FN, ...)                                             \
+    do {                                                                \
+        if (dtype == RECSA_BF16 && D_ == 128) return FN<128, 1>(__VA_ARGS__); \
+        if (dtype == RECSA_BF16 && D_ == 64) return FN<64, 1>(__VA_ARGS__);   \
+        if (dtype == RECSA_F32 && D_ == 128) return FN<128, 2>(__VA_ARGS__);  \
+        if (dtype == RECSA_F32 && D_ == 64) return FN<64, 2>(__VA_ARGS__);    \
+        return cudaErrorInvalidValue;                                   \
+    } while (0)
+
+cudaError_t kv4_prepare_attend(int dtype, int D_) { KV4_ATTEND(prepare_impl); }
+
+cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
+                              const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s) {
+    NvtxRange nv("recsa kv4 attend");
+    const int D_ = c.D;
+    KV4_ATTEND(attend_impl, c, qv, sc, maps, chunk, s);
+}
+
+cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
+                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s) {
+    NvtxRange nv("recsa kv4 weights");
+    const int D_ = c.D;
+    KV4_ATTEND(weights_impl, c, qv, sc, maps, chunk, s);
+}
+
+}  // namespace recsa

@@ -65,6 +65,23 @@ class RecsaTreeInfoC(ctypes.Structure):
     ]
 
 
+class RecsaKV4InfoC(ctypes.Structure):
+    _fields_ = [
+        ("capacity", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("batch", ctypes.c_int32),
+        ("max_queries", ctypes.c_int32),
+        ("k_codes", ctypes.c_int64),
+        ("v_codes", ctypes.c_int64),
+        ("k_params", ctypes.c_int64),
+        ("v_params", ctypes.c_int64),
+        ("positions", ctypes.c_int64),
+        ("weights", ctypes.c_int64),
+        ("lengths", ctypes.c_int64),
+        ("tokens_seen", ctypes.c_int64),
+    ]
+
+
 def _load():
     # RECSA_LIBRARY selects another build of this library (the bounds-checked
     # librecsa_bounds.so in its tests); there is no fallback when it is missing
@@ -95,6 +112,19 @@ def _load():
         "recsa_offload_staging_bytes": [ctypes.POINTER(RecsaConfigC), I32, ctypes.POINTER(SZ)],
         "recsa_tree_set_offload_staging": [P, P, SZ],
         "recsa_tree_free": [P],
+        "recsa_kv4_query_sizes": [ctypes.POINTER(RecsaConfigC), I64, I32, I32, ctypes.POINTER(SZ),
+                                  ctypes.POINTER(SZ)],
+        "recsa_kv4_init": [ctypes.POINTER(RecsaConfigC), I64, I32, I32, P, SZ, P, SZ, P,
+                           ctypes.POINTER(P)],
+        "recsa_kv4_build": [P, P, P, ctypes.POINTER(I64), ctypes.POINTER(I64), P],
+        "recsa_kv4_append": [P, P, P, I32, P, P],
+        "recsa_kv4_decode": [P, P, P, I32, P],
+        "recsa_kv4_prefill_chunk": [P, P, I32, P, P, I32, P],
+        "recsa_kv4_evict": [P, I64, I64, I64, P],
+        "recsa_kv4_read": [P, I64, I64, P, P, P],
+        "recsa_kv4_get_status": [P, P],
+        "recsa_kv4_info": [P, ctypes.POINTER(RecsaKV4InfoC)],
+        "recsa_kv4_free": [P],
         "recsa_status_str": [I32],
     }
     for name, args in sig.items():
@@ -343,3 +373,163 @@ class RecsaTree:
         K = self.levels[ko.value: ko.value + n * es].view(self.cfg.torch_dtype).view(shape)
         V = self.levels[vo.value: vo.value + n * es].view(self.cfg.torch_dtype).view(shape)
         return K, V
+
+
+def recsa_kv4_query_sizes(cfg: Config, capacity: int, batch: int, max_queries: int):
+    cb, wb = ctypes.c_size_t(), ctypes.c_size_t()
+    c = cfg.to_c()
+    _check(lib.recsa_kv4_query_sizes(ctypes.byref(c), capacity, batch, max_queries,
+                                     ctypes.byref(cb), ctypes.byref(wb)), "recsa_kv4_query_sizes")
+    return cb.value, wb.value
+
+
+class RecsaKV4:
+    """A 4-bit KV cache bound to torch-allocated device buffers (see the header).
+
+    cfg: head_dim, n_q_heads, n_kv_heads, dtype and scale are used.  max_queries: query
+    rows of one wave of a chunk over all sequences (batch by default).
+    """
+
+    def __init__(self, cfg: Config, capacity: int, batch: int, max_queries: int | None = None,
+                 device="cuda", stream=None):
+        self.cfg = cfg
+        self.capacity, self.batch = capacity, batch
+        self.max_queries = max_queries or batch
+        cb, wb = recsa_kv4_query_sizes(cfg, capacity, batch, self.max_queries)
+        self.cache = torch.empty(cb, dtype=torch.uint8, device=device)
+        self.workspace = torch.empty(wb, dtype=torch.uint8, device=device)
+        self.device = self.cache.device
+        c = cfg.to_c()
+        h = ctypes.c_void_p()
+        _check(lib.recsa_kv4_init(ctypes.byref(c), capacity, batch, self.max_queries,
+                                  _ptr(self.cache), cb, _ptr(self.workspace), wb,
+                                  self._on(stream), ctypes.byref(h)), "recsa_kv4_init")
+        self.handle = h
+        self.info = RecsaKV4InfoC()
+        _check(lib.recsa_kv4_info(h, ctypes.byref(self.info)), "recsa_kv4_info")
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value:
+            lib.recsa_kv4_free(h)
+            self.handle = None
+
+    def _on(self, stream):
+        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _rows(self, t: torch.Tensor, shape, name: str):
+        if t.dtype != self.cfg.torch_dtype or t.device != self.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, expected "
+                             f"{self.cfg.torch_dtype} on {self.device}")
+        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor of shape {tuple(shape)} expected, got "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+
+    def _counts(self, counts):
+        if counts is not None and (counts.dtype != torch.int32 or counts.device != self.device
+                                   or tuple(counts.shape) != (self.batch,)
+                                   or not counts.is_contiguous()):
+            raise ValueError(f"counts: contiguous int32 [{self.batch}] on {self.device} expected")
+        return _ptr(counts)
+
+    # --- the C-ABI calls -------------------------------------------------------
+    def recsa_kv4_build(self, k: torch.Tensor, v: torch.Tensor, lengths, stream=None):
+        """k, v: [batch][Hkv][T][d] with d contiguous, equal strides, T >= max(lengths)."""
+        lens = [int(x) for x in lengths]
+        c = self.cfg
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype != c.torch_dtype or t.device != self.device:
+                raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {c.torch_dtype} on "
+                                 f"{self.device}")
+            if t.dim() != 4 or t.shape[:2] != (self.batch, c.n_kv_heads) or \
+                    t.shape[3] != c.head_dim or t.stride(3) != 1:
+                raise ValueError(f"{name}: [batch][Hkv][T][d] with contiguous d expected, got "
+                                 f"{tuple(t.shape)}")
+        if len(lens) != self.batch or max(lens) > min(k.shape[2], v.shape[2]):
+            raise ValueError(f"lengths {lens}: {self.batch} of them, at most the rows given")
+        if k.stride() != v.stride():
+            raise ValueError("k and v must have the same strides")
+        arr = (ctypes.c_int64 * self.batch)(*lens)
+        # a dim of one element has no stride that matters: the library checks all three
+        st = [s if n > 1 else c.head_dim for s, n in zip(k.stride()[:3], k.shape[:3])]
+        strides = (ctypes.c_int64 * 3)(*st)
+        _check(lib.recsa_kv4_build(self.handle, _ptr(k), _ptr(v), strides, arr, self._on(stream)),
+               "recsa_kv4_build")
+
+    def recsa_kv4_append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts=None, stream=None):
+        n = k_new.shape[2]
+        shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
+        self._rows(k_new, shape, "k_new")
+        self._rows(v_new, shape, "v_new")
+        _check(lib.recsa_kv4_append(self.handle, _ptr(k_new), _ptr(v_new), n, self._counts(counts),
+                                    self._on(stream)), "recsa_kv4_append")
+
+    def recsa_kv4_decode(self, q: torch.Tensor, out: torch.Tensor, accumulate: bool = False,
+                         stream=None):
+        shape = (self.batch, self.cfg.n_q_heads, self.cfg.head_dim)
+        self._rows(q, shape, "q")
+        self._rows(out, shape, "out")
+        _check(lib.recsa_kv4_decode(self.handle, _ptr(q), _ptr(out), int(bool(accumulate)),
+                                    self._on(stream)), "recsa_kv4_decode")
+
+    def recsa_kv4_prefill_chunk(self, Q: torch.Tensor, O: torch.Tensor, counts=None,
+                                accumulate_rows: int = 0, stream=None):
+        n = Q.shape[1]
+        shape = (self.batch, n, self.cfg.n_q_heads, self.cfg.head_dim)
+        self._rows(Q, shape, "Q")
+        self._rows(O, shape, "O")
+        _check(lib.recsa_kv4_prefill_chunk(self.handle, _ptr(Q), n, self._counts(counts), _ptr(O),
+                                           accumulate_rows, self._on(stream)),
+               "recsa_kv4_prefill_chunk")
+
+    def recsa_kv4_evict(self, budget: int, n_first: int = 0, n_recent: int = 0, stream=None):
+        _check(lib.recsa_kv4_evict(self.handle, budget, n_first, n_recent, self._on(stream)),
+               "recsa_kv4_evict")
+
+    def recsa_kv4_read(self, start: int, n: int, k_out=None, v_out=None, stream=None):
+        shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None:
+                self._rows(t, shape, name)
+        _check(lib.recsa_kv4_read(self.handle, start, n, _ptr(k_out), _ptr(v_out),
+                                  self._on(stream)), "recsa_kv4_read")
+
+    def recsa_kv4_get_status(self, stream=None) -> int:
+        return lib.recsa_kv4_get_status(self.handle, self._on(stream))
+
+    # --- conveniences (allocation + views only) -------------------------------
+    def decode(self, q: torch.Tensor, accumulate: bool = False, stream=None):
+        out = torch.empty_like(q)
+        self.recsa_kv4_decode(q, out, accumulate, stream)
+        return out
+
+    def prefill(self, Q: torch.Tensor, counts=None, accumulate_rows: int = 0, stream=None):
+        """Rows past a sequence's count are zeros."""
+        O = torch.empty_like(Q) if counts is None else torch.zeros_like(Q)
+        self.recsa_kv4_prefill_chunk(Q, O, counts, accumulate_rows, stream)
+        return O
+
+    def read(self, start: int, n: int, stream=None):
+        k = torch.empty(self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim,
+                        dtype=self.cfg.torch_dtype, device=self.device)
+        v = torch.empty_like(k)
+        self.recsa_kv4_read(start, n, k, v, stream)
+        return k, v
+
+    def _table(self, buf: torch.Tensor, offset: int, shape, dtype):
+        n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        return buf[offset: offset + n].view(dtype).view(shape)
+
+    def positions(self):
+        """int32 view [batch][Hkv][rows] of the slots' token positions (0 past the length)."""
+        return self._table(self.cache, self.info.positions,
+                           (self.batch, self.cfg.n_kv_heads, self.info.rows), torch.int32)
+
+    def weights(self):
+        """fp32 view [batch][Hkv][rows] of the accumulated weights (0 past the length)."""
+        return self._table(self.cache, self.info.weights,
+                           (self.batch, self.cfg.n_kv_heads, self.info.rows), torch.float32)
+
+    def lengths(self):
+        """int64 view [batch] of the device-side lengths."""
+        return self._table(self.workspace, self.info.lengths, (self.batch,), torch.int64)
