@@ -7,10 +7,12 @@
 // flops on them, so it is bound by the cache read; dequantising every code to a float
 // would cost more issue slots than the bytes take to arrive, so no code is dequantised:
 //
-//   * A nibble in place in a 16-bit half is a subnormal fp16 number, code * 2^-24 (or
-//     code * 2^-20 for the nibble above it), exact.  `word & 0x000f000f` is therefore two
-//     operand elements of mma.sync.m16n8k16 (fp16 in, fp32 accumulators), and a word of
-//     eight codes costs four ANDs and one shift.
+//   * Codes are the operands of mma.sync.m16n8k16 (fp16 in, fp32 accumulators).  A nibble in
+//     place in a 16-bit half is a subnormal fp16 number, code * 2^-24 (or code * 2^-20 for the
+//     nibble above it), exact: `word & 0x000f000f` is two operand elements.  The products
+//     of subnormal operands are aligned by their unnormalised exponent, which leaves about
+//     18 bits of a sum: enough beside bf16 (2^-9), used there for K.  Elsewhere the nibble
+//     is joined to an exponent (1024 + code) and 1032 subtracted: code - 8, a normal number.
 //   * Scores: S[16 tokens x 8 columns] per group of 32 dims from two MMAs with the codes
 //     as A (ldmatrix of the packed rows) and q as B, then s and lo enter in fp32:
 //     S += s_tg * (code . q)_tg + lo_tg * (sum of q over g).
@@ -99,18 +101,19 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
 }
-// Both halves minus 8 codes (low nibble: 8 * 2^-24; the nibble above it: 8 * 2^-20), exact.
+// code - 8 of the low nibble of both halves as normal fp16 numbers: 1024 + code, less 1032.
 __device__ __forceinline__ uint32_t centre_lo(uint32_t x) {
-    __half2 a = *reinterpret_cast<__half2*>(&x);
-    const uint32_t m = 0x80088008u;
-    a = __hadd2(a, *reinterpret_cast<const __half2*>(&m));
-    return *reinterpret_cast<uint32_t*>(&a);
+    x = (x & 0x000f000fu) | 0x64006400u;
+    const uint32_t m = 0xe408e408u;
+    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&m));
+    return *reinterpret_cast<const uint32_t*>(&a);
 }
+// The same of the nibble above it: 64 + code, less 72.
 __device__ __forceinline__ uint32_t centre_hi(uint32_t x) {
-    __half2 a = *reinterpret_cast<__half2*>(&x);
-    const uint32_t m = 0x80808080u;
-    a = __hadd2(a, *reinterpret_cast<const __half2*>(&m));
-    return *reinterpret_cast<uint32_t*>(&a);
+    x = (x & 0x00f000f0u) | 0x54005400u;
+    const uint32_t m = 0xd480d480u;
+    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&m));
+    return *reinterpret_cast<const uint32_t*>(&a);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -178,9 +181,9 @@ __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query
         // the sum over the group's 32 / E lanes
 #pragma unroll
         for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (lane % (32 / E) == 0) rs.sum[r][lane / (32 / E)] = sum * 0x1p-24f;
+        if (lane % (32 / E) == 0) rs.sum[r][lane / (32 / E)] = T == 1 ? sum * 0x1p-24f : sum;
         if (lane == 0) {
-            rs.scale[r] = fminf(c.scale * 1.4426950408889634f * pow2i(ex - 10) * 0x1p24f, 3e38f);
+            rs.scale[r] = fminf(c.scale * 1.4426950408889634f * pow2i(ex - 10) * (T == 1 ? 0x1p24f : 1.0f), 3e38f);
             rs.lim[r] = live ? (int)(seen - n_b + i) : -1;
         }
         // dim 8t + k of a group (k < 8) sits in 16-bit unit (k >> 1 with the pairs
@@ -189,7 +192,7 @@ __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int dim = lane * E + e, grp = dim / 32, t = (dim / 8) & 3, k = dim & 7;
-            const float y = (k & 1) ? x[e] * 0.0625f : x[e];
+            const float y = T == 1 && (k & 1) ? x[e] * 0.0625f : x[e];
             const int reg = k & 3, half = k >> 2;
             if constexpr (T == 1) {
                 const int l = (r & 7) * 4 + t;
@@ -238,17 +241,19 @@ __device__ __forceinline__ void scores16(float (&sc)[NCS][2 * (2 / T)], uint32_t
         for (int jj = 0; jj < 2; ++jj) {
             const int j = j2 + jj;
             const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
-            uint32_t a[8] = {wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                             (wa >> 8) & 0x000f000fu, (wb >> 8) & 0x000f000fu,
-                             (wa >> 8) & 0x00f000f0u, (wb >> 8) & 0x00f000f0u};
+            uint32_t a[8];
             float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
             float o0 = kv4_off(p0[j]), o1 = kv4_off(p1[j]);
-            if constexpr (T == 2) {
-                // fp32: centred codes, so that the two terms of a score stay small
-                a[0] = centre_lo(a[0]); a[1] = centre_lo(a[1]);
-                a[2] = centre_hi(a[2]); a[3] = centre_hi(a[3]);
-                a[4] = centre_lo(a[4]); a[5] = centre_lo(a[5]);
-                a[6] = centre_hi(a[6]); a[7] = centre_hi(a[7]);
+            if constexpr (T == 1) {
+                a[0] = wa & 0x000f000fu; a[1] = wb & 0x000f000fu;
+                a[2] = wa & 0x00f000f0u; a[3] = wb & 0x00f000f0u;
+                a[4] = (wa >> 8) & 0x000f000fu; a[5] = (wb >> 8) & 0x000f000fu;
+                a[6] = (wa >> 8) & 0x00f000f0u; a[7] = (wb >> 8) & 0x00f000f0u;
+            } else {
+                a[0] = centre_lo(wa); a[1] = centre_lo(wb);
+                a[2] = centre_hi(wa); a[3] = centre_hi(wb);
+                a[4] = centre_lo(wa >> 8); a[5] = centre_lo(wb >> 8);
+                a[6] = centre_hi(wa >> 8); a[7] = centre_hi(wb >> 8);
                 o0 = fmaf(8.0f, s0, o0);
                 o1 = fmaf(8.0f, s1, o1);
             }
@@ -543,14 +548,14 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         const int j = j2 + jj;
                         const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
                         // dims 4g + k of the group, tokens 2t, 2t + 1 (wa) and + 8 (wb)
-                        const uint32_t a0 = centre_lo(wa & 0x000f000fu);
-                        const uint32_t a1 = centre_hi(wa & 0x00f000f0u);
-                        const uint32_t a2 = centre_lo(wb & 0x000f000fu);
-                        const uint32_t a3 = centre_hi(wb & 0x00f000f0u);
-                        const uint32_t a4 = centre_lo((wa >> 8) & 0x000f000fu);
-                        const uint32_t a5 = centre_hi((wa >> 8) & 0x00f000f0u);
-                        const uint32_t a6 = centre_lo((wb >> 8) & 0x000f000fu);
-                        const uint32_t a7 = centre_hi((wb >> 8) & 0x00f000f0u);
+                        const uint32_t a0 = centre_lo(wa);
+                        const uint32_t a1 = centre_hi(wa);
+                        const uint32_t a2 = centre_lo(wb);
+                        const uint32_t a3 = centre_hi(wb);
+                        const uint32_t a4 = centre_lo(wa >> 8);
+                        const uint32_t a5 = centre_hi(wa >> 8);
+                        const uint32_t a6 = centre_lo(wb >> 8);
+                        const uint32_t a7 = centre_hi(wb >> 8);
                         const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
                         float c0 = fmaf(8.0f, s0, kv4_off(p0[j]));
                         float c1 = fmaf(8.0f, s1, kv4_off(p1[j]));
@@ -627,19 +632,19 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                     float4 v;
                     if constexpr (T == 1) {
                         v.x = O[cs][j][0][e];
-                        v.y = O[cs][j][0][2 + e] * 0.0625f;
+                        v.y = O[cs][j][0][2 + e];
                         v.z = O[cs][j][1][e];
-                        v.w = O[cs][j][1][2 + e] * 0.0625f;
+                        v.w = O[cs][j][1][2 + e];
                     } else {
                         v.x = fmaf(O[cs][j][0][1], 1.0f / kLowUp, O[cs][j][0][0]);
-                        v.y = fmaf(O[cs][j][0][3], 1.0f / kLowUp, O[cs][j][0][2]) * 0.0625f;
+                        v.y = fmaf(O[cs][j][0][3], 1.0f / kLowUp, O[cs][j][0][2]);
                         v.z = fmaf(O[cs][j][1][1], 1.0f / kLowUp, O[cs][j][1][0]);
-                        v.w = fmaf(O[cs][j][1][3], 1.0f / kLowUp, O[cs][j][1][2]) * 0.0625f;
+                        v.w = fmaf(O[cs][j][1][3], 1.0f / kLowUp, O[cs][j][1][2]);
                     }
-                    v.x = fmaf(v.x * 0x1p24f, vinv, bs);
-                    v.y = fmaf(v.y * 0x1p24f, vinv, bs);
-                    v.z = fmaf(v.z * 0x1p24f, vinv, bs);
-                    v.w = fmaf(v.w * 0x1p24f, vinv, bs);
+                    v.x = fmaf(v.x, vinv, bs);
+                    v.y = fmaf(v.y, vinv, bs);
+                    v.z = fmaf(v.z, vinv, bs);
+                    v.w = fmaf(v.w, vinv, bs);
                     *reinterpret_cast<float4*>(red + ((size_t)warp * RB + r) * D + j * 32 + g * 4) = v;
                 }
             }
