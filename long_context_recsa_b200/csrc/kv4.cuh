@@ -53,7 +53,7 @@ struct Kv4Source {
 // Scratch of the attention kernels.
 struct Kv4Scratch {
     float* part;             // [2 * grid][rows a block][D + 2] split-softmax partials
-    uint32_t* ucnt;          // [grid] CTAs that finished a split unit (left at 0)
+    uint32_t* ucnt;          // [3 * grid] arrivals at the joins of split units (left at 0)
     float* lse;              // [U][rows] log2 of each row's softmax sum
 };
 
@@ -76,8 +76,7 @@ cudaError_t kv4_launch_read(const Kv4View& c, int64_t start, int64_t n, void* k,
                             cudaStream_t s);
 cudaError_t kv4_launch_evict(const Kv4View& c, int64_t budget, int64_t n_first, int64_t n_recent,
                              int32_t* lists, cudaStream_t s);
-int kv4_attend_grid();                                  // CTAs of the largest attention launch
-int kv4_attend_rows(int dtype, int G, int rows);        // rows a block of rows
+int kv4_attend_counters();                              // words of Kv4Scratch::ucnt
 size_t kv4_attend_part_floats(int D);                   // floats of Kv4Scratch::part
 cudaError_t kv4_prepare_attend(int dtype, int D);
 cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,

@@ -55,7 +55,7 @@ recsa_status kv4_layout(const recsa_config* c, int64_t cap, int B, int Qmax, Kv4
     L->o_seen = w;   w = up256(w + sizeof(int64_t) * B);
     L->o_kmax = w;   w = up256(w + sizeof(uint32_t) * L->U);
     L->o_vmax = w;   w = up256(w + sizeof(uint32_t) * L->U);
-    L->o_ucnt = w;   w = up256(w + sizeof(uint32_t) * kv4_attend_grid());
+    L->o_ucnt = w;   w = up256(w + sizeof(uint32_t) * kv4_attend_counters());
     L->o_lse = w;    w = up256(w + sizeof(float) * (size_t)Qmax * c->n_q_heads);
     L->o_part = w;   w = up256(w + sizeof(float) * kv4_attend_part_floats(L->D));
     L->o_lists = w;  w = up256(w + sizeof(int32_t) * rows);
@@ -210,7 +210,7 @@ recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t b
                              !encode_codes(&t->maps.v, c.vc, L.D, L.R, L.U, 32)))
         e = cudaErrorNotSupported;
     if (e == cudaSuccess)
-        e = cudaMemsetAsync(t->sc.ucnt, 0, sizeof(uint32_t) * kv4_attend_grid(), s);
+        e = cudaMemsetAsync(t->sc.ucnt, 0, sizeof(uint32_t) * kv4_attend_counters(), s);
     if (e == cudaSuccess) e = kv4_launch_clear(c, s);
     if (e != cudaSuccess) {
         free(t);

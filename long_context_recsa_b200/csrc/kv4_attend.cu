@@ -33,7 +33,8 @@
 // of 32 tokens.  All tiles of all units form one list, cut evenly over a persistent grid
 // (so ragged batches balance); a CTA's warps take its tiles in turn, each with its own ring
 // of TMA stages, running maximum and accumulators, and meet only at the end of a unit.  A
-// unit cut over several CTAs is joined by the last of them, in the order of the CTAs.
+// unit cut over several CTAs is joined by the last of each 16 and then by the last of those
+// (one CTA joining all 74 of a unit took longer than the unit).
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -47,6 +48,7 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = kAttendWarps * 32;
 constexpr int kStagesKv4 = 2;
 constexpr int kGridMax = 148 * 4;
+constexpr int kJoin = 16;            // partial results that one CTA joins
 constexpr float kSlack = 6.0f;       // p may reach 2^6 before the running maximum moves
 constexpr float kLowUp = 2048.0f;    // fp32 tensors: scale of the low part of P' (its own column)
 
@@ -670,8 +672,9 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                 sc_.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] =
                     ls > 0.0f || ls != ls ? mx + log2f(ls) : INFINITY;
         };
-        float* part = whole ? nullptr
-                            : sc_.part + (size_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * RB * (D + 2);
+        auto slot = [&](int64_t cta) { return 2 * cta + (cta == cta0 ? 1 : 0); };
+        auto part_of = [&](int64_t cta) { return sc_.part + (size_t)slot(cta) * RB * (D + 2); };
+        float* part = whole ? nullptr : part_of(blockIdx.x);
         for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
             float mx = red_m[0][r];
@@ -700,37 +703,73 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
             }
         }
         if (!whole) {
-            // the last CTA of the unit joins the partials in the order of the CTAs
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                last_flag = atomicAdd(&sc_.ucnt[cta0], 1u) == (uint32_t)(cta1 - cta0);
-                if (last_flag) sc_.ucnt[cta0] = 0;
-            }
-            __syncthreads();
-            if (last_flag) {
+            // Joined in groups of kJoin CTAs, each by the last of its CTAs to arrive; then
+            // the groups' results likewise.  Either way the sums follow the CTAs' order.
+            float* fac = reinterpret_cast<float*>(ring);   // [n][RB], over the warps' results
+            auto last_of = [&](uint32_t* counter, uint32_t n) {
                 __threadfence();
-                auto slot = [&](int64_t cta) {
-                    return sc_.part + (size_t)(2 * cta + (cta == cta0 ? 1 : 0)) * RB * (D + 2);
-                };
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    last_flag = atomicAdd(counter, 1u) == n - 1;
+                    if (last_flag) *counter = 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                return last_flag != 0;
+            };
+            // partials of CTAs first, first + step, ..: into the first's slot, or stored
+            auto join = [&](int64_t first, int64_t step, int n, bool store) {
+                for (int i = threadIdx.x; i < n * RB; i += kAttendThreads) {
+                    const float* p = part_of(first + (i / RB) * step) + RB * D + i % RB;
+                    fac[i] = __ldcg(p);
+                    fac[n * RB + i] = __ldcg(p + RB);
+                }
+                __syncthreads();
+                if (threadIdx.x < RB) {
+                    const int r = threadIdx.x;
+                    float mx = kKv4MinLog2, ls = 0.0f;
+                    for (int k = 0; k < n; ++k) mx = fmaxf(mx, fac[k * RB + r]);
+                    for (int k = 0; k < n; ++k) {
+                        const float f = ex2(fac[k * RB + r] - mx);
+                        ls = fmaf(f, fac[n * RB + k * RB + r], ls);
+                        fac[k * RB + r] = f;
+                    }
+                    red_m[0][r] = mx;
+                    red_l[0][r] = ls;
+                }
+                __syncthreads();
+                float* to = part_of(first);
                 for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
                     const int r = i / (D / 4), d4 = i % (D / 4);
-                    float mx = kKv4MinLog2;
-                    for (int64_t k = cta0; k <= cta1; ++k) mx = fmaxf(mx, __ldcg(slot(k) + RB * D + r));
-                    float ls = 0.0f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int64_t k = cta0; k <= cta1; ++k) {
-                        const float* p = slot(k);
-                        const float f = ex2(__ldcg(p + RB * D + r) - mx);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d4 * 4));
-                        ls = fmaf(f, __ldcg(p + RB * D + RB + r), ls);
+#pragma unroll 8
+                    for (int k = 0; k < n; ++k) {
+                        const float f = fac[k * RB + r];
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(
+                            part_of(first + k * step) + r * D + d4 * 4));
                         v.x = fmaf(f, x.x, v.x);
                         v.y = fmaf(f, x.y, v.y);
                         v.z = fmaf(f, x.z, v.z);
                         v.w = fmaf(f, x.w, v.w);
                     }
-                    store_row(r, d4, v, mx, ls);
+                    if (store) {
+                        store_row(r, d4, v, red_m[0][r], red_l[0][r]);
+                    } else {
+                        *reinterpret_cast<float4*>(to + r * D + d4 * 4) = v;
+                        if (d4 == 0) {
+                            to[RB * D + r] = red_m[0][r];
+                            to[RB * D + RB + r] = red_l[0][r];
+                        }
+                    }
                 }
+            };
+            const int n = (int)(cta1 - cta0) + 1, groups = (n + kJoin - 1) / kJoin;
+            const int64_t first = cta0 + ((int64_t)blockIdx.x - cta0) / kJoin * kJoin;
+            const int members = (int)(cta1 - first) + 1 < kJoin ? (int)(cta1 - first) + 1 : kJoin;
+            if (last_of(sc_.ucnt + slot(first), members)) {
+                join(first, 1, members, groups == 1);
+                if (groups > 1 && last_of(sc_.ucnt + 2 * kGridMax + cta0, groups))
+                    join(cta0, kJoin, groups, true);
             }
         }
         at += tile1 - tile0;
@@ -976,6 +1015,7 @@ cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch&
 }  // namespace
 
 int kv4_attend_grid() { return kGridMax; }
+int kv4_attend_counters() { return 3 * kGridMax; }
 size_t kv4_attend_part_floats(int D) { return (size_t)2 * kGridMax * 32 * (D + 2); }
 
 #define KV4_ATTEND(FN, ...)                                             \
