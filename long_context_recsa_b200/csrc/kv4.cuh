@@ -48,6 +48,7 @@ struct Kv4Source {
     int64_t n;               // rows a sequence (append); the largest length (build)
     const int32_t* counts;   // append: rows in use of each sequence, or nullptr for n
     int append;
+    int tiles;               // rows of a lane (set by the launcher)
 };
 
 // Scratch of the attention kernels.
@@ -74,6 +75,7 @@ cudaError_t kv4_launch_build(const Kv4View& c, const Kv4Source& src, const Kv4Le
 cudaError_t kv4_launch_append(const Kv4View& c, const Kv4Source& src, int dtype, cudaStream_t s);
 cudaError_t kv4_launch_read(const Kv4View& c, int64_t start, int64_t n, void* k, void* v, int dtype,
                             cudaStream_t s);
+cudaError_t kv4_prepare_evict(const Kv4View& c);
 cudaError_t kv4_launch_evict(const Kv4View& c, int64_t budget, int64_t n_first, int64_t n_recent,
                              int32_t* lists, cudaStream_t s);
 int kv4_attend_counters();                              // words of Kv4Scratch::ucnt

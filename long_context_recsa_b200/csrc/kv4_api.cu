@@ -206,6 +206,7 @@ recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t b
     OnDevice on(dev);
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = on.ok ? kv4_prepare_attend(cfg->dtype, L.D) : cudaErrorInvalidDevice;
+    if (e == cudaSuccess) e = kv4_prepare_evict(c);
     if (e == cudaSuccess && (!encode_codes(&t->maps.k, c.kc, L.D, L.R, L.U, 32) ||
                              !encode_codes(&t->maps.v, c.vc, L.D, L.R, L.U, 32)))
         e = cudaErrorNotSupported;

@@ -1014,7 +1014,6 @@ cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch&
 
 }  // namespace
 
-int kv4_attend_grid() { return kGridMax; }
 int kv4_attend_counters() { return 3 * kGridMax; }
 size_t kv4_attend_part_floats(int D) { return (size_t)2 * kGridMax * 32 * (D + 2); }
 

@@ -1,10 +1,10 @@
 // Writing and reading rows of the 4-bit KV cache: quantisation (build, append) and
 // dequantisation (read).  The format is in kv4.cuh.
 //
-// All three are bound by memory: a bf16 row of d = 128 is 256 bytes in and 80 out.  Four
-// lanes own a group (8 dims each, one 16-byte load of bf16), so a group's minimum and
-// maximum take two shuffles, a lane's 8 codes are one word, and a warp's stores of codes
-// are whole 128-byte lines.  Four rows a thread are loaded before the first is used.
+// All three are bound by memory if the quantisation takes few instructions: a bf16 row of
+// d = 128 is 256 bytes in and 80 out.  Two lanes own
+// a group (16 dims each), so what is done once a group costs a sixteenth of it a dim, and
+// the group's minimum and maximum take one exchange; arithmetic goes two dims at a time.
 #include "kv4.cuh"
 
 namespace recsa {
@@ -12,87 +12,179 @@ namespace recsa {
 namespace {
 
 constexpr int kThreadsRows = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;           // rows of a lane that are loaded before the first is used
+constexpr int kTilesRows = 8;        // rows of a lane in all, at most
+constexpr int kReadRows = 4;         // rows of a lane in the read back
+
+// 16 dims of a row as they are stored: two 16-byte words of bf16, four of fp32.
+template <typename T> struct Raw { uint4 a[(int)sizeof(T)]; };
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-    load16_nc<__nv_bfloat16>(p, x);
+__device__ __forceinline__ void load_raw(Raw<T>& r, const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) r.a[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-    load16_nc<float>(p, x);
-    load16_nc<float>(p + 4, x + 4);
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {   // of two bf16
+    uint32_t y;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
+// The 16 values, and the smallest and largest of the group (lanes l and l ^ 1); both are
+// NaN if one of the group is.
+__device__ __forceinline__ void spread(const Raw<__nv_bfloat16>& r, float2 (&x)[8], float& mn,
+                                       float& mx) {
+    const uint32_t w[8] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w,
+                           r.a[1].x, r.a[1].y, r.a[1].z, r.a[1].w};
+    uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        if (i > 0) {
+            lo = min2_nan(lo, w[i]);
+            hi = max2_nan(hi, w[i]);
+        }
+    }
+    hi ^= 0x80008000u;                   // the largest as the smallest of the negated: one word
+    uint32_t both = min2_nan(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    both = min2_nan(both, __shfl_xor_sync(kFull, both, 1));
+    mn = __uint_as_float(both << 16);
+    mx = -__uint_as_float(both & 0xffff0000u);
+}
+__device__ __forceinline__ void spread(const Raw<float>& r, float2 (&x)[8], float& mn, float& mx) {
+    float lo = __uint_as_float(r.a[0].x), hi = -lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = make_float2(__uint_as_float(r.a[i].x), __uint_as_float(r.a[i].y));
+        x[2 * i + 1] = make_float2(__uint_as_float(r.a[i].z), __uint_as_float(r.a[i].w));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo = min_nan(min_nan(lo, x[i].x), x[i].y);
+        hi = min_nan(min_nan(hi, -x[i].x), -x[i].y);
+    }
+    mn = min_nan(lo, __shfl_xor_sync(kFull, lo, 1));
+    mx = -min_nan(hi, __shfl_xor_sync(kFull, hi, 1));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return y;
+}
+__device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
 
 // bf16 bits (in the high half) of the largest bf16 <= x.
 __device__ __forceinline__ uint32_t bf16_floor(float x) {
     const uint32_t u = __float_as_uint(x), cut = u & 0xffff0000u;
     return ((u >> 31) && u != cut) ? cut + 0x10000u : cut;
 }
-// bf16 bits (in the high half) of the smallest bf16 >= x, x >= 0.
-__device__ __forceinline__ uint32_t bf16_ceil(double x) {
-    uint32_t u = __float_as_uint(__double2float_ru(x));
-    return (u & 0xffffu) ? (u & 0xffff0000u) + 0x10000u : u;
+
+// 1 where x - lo < (k - 1/2) s in real arithmetic, or equal with k odd: code k is one too high.
+__device__ __forceinline__ uint32_t too_high(float x, float lo, float k, float s) {
+    const float half = (k - 0.5f) * s;
+    if (__fsub_rd(x, lo) < half) return 1u;
+    return __fsub_ru(x, lo) > half ? 0u : (uint32_t)((int)k & 1);
 }
 
-// Quantises the 8 dims of this lane; the group's four lanes are l, l^1, l^2, l^3.
-// `code` gets the lane's 8 nibbles, `par` the group's parameter word; returns the
-// largest |value| of the group (0 for a group of NaN).
+// Quantises the 16 dims of this lane (spread() above has the group's extremes).  `code`
+// gets the lane's 16 nibbles, `par` the group's parameter word; returns the largest |value|
+// of the group (0 for a group of NaN).
 //
-// Codes follow the definition in real arithmetic: (x - lo) / s is formed in fp32 (off
-// by less than 1e-5), and where that is within 1e-4 of a half, the sign of
-// (x - lo) - (k + 1/2) s in fp64 decides.
-__device__ __forceinline__ float quantize8(const float (&x)[8], uint32_t& code, uint32_t& par) {
-    float mn = x[0], mx = x[0], bad = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-        bad += x[i] * 0.0f;              // NaN for a NaN or an infinity
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-        bad += __shfl_xor_sync(kFull, bad, o);
-    }
+// Everything is decided as in real arithmetic, with fp32 operations only (fp64 ones took
+// 397 us instead of 208 at 131072 x 8 bf16 rows).  A difference rounded up (down) is the
+// smallest (largest) fp32 number not below (above) the real one, so it compares with a
+// number of fp32 as the real difference does:
+//   s: the smallest bf16 with 15 s >= mx - lo; 15 s is exact.  A product with 1 / 15 is off
+//      by less than a step of bf16, two corrections suffice.
+//   codes: the quotient is formed a few 1e-7 too large, so that rounding it may give a code
+//      one too high but never one too low; the remainder x - lo - code s shows where that
+//      may be (bf16 values lie on ties often), and too_high() decides.
+__device__ __forceinline__ float quantize16(const float2 (&x)[8], float mn, float mx, uint2& code,
+                                            uint32_t& par) {
     const uint32_t lob = bf16_floor(mn);
     const float lo = __uint_as_float(lob);
-    const uint32_t sb = bf16_ceil(((double)mx - (double)lo) / 15.0);
-    const float s = __uint_as_float(sb);
-    code = 0;
-    if (bad != 0.0f || !(fabsf(lo) <= 3.4e38f) || !(s <= 3.4e38f)) {
-        par = 0x7fc00000u;               // lo = NaN, s = 0
-        return 0.0f;
+    const float range = __fsub_ru(mx, lo);
+    uint32_t sb = __float_as_uint(range * (1.0f / 15.0f)) & 0xffff0000u;
+    if (__uint_as_float(sb) * 15.0f < range) sb += 0x10000u;
+    if (__uint_as_float(sb) * 15.0f < range) sb += 0x10000u;
+    if (range > 1e38f) {
+        // the range itself may pass fp32
+        sb = __float_as_uint(__double2float_ru(((double)mx - (double)lo) / 15.0));
+        if (sb & 0xffffu) sb = (sb & 0xffff0000u) + 0x10000u;
     }
-    par = (sb >> 16) | lob;
-    if (s < 1e-30f) {
-        // tiny steps: 1 / s may overflow fp32
-        if (s > 0.0f)
+    const float s = __uint_as_float(sb);
+    uint32_t c[2] = {0, 0};
+    float big = 0.0f;
+    par = 0x7fc00000u;                   // lo = NaN, s = 0: a group that cannot be held
+    if (fabsf(lo) <= 3.4e38f && s <= 3.4e38f) {
+        par = (sb >> 16) | lob;
+        big = fmaxf(fabsf(lo), fabsf(fmaf(s, 15.0f, lo)));
+        if (s >= 1e-30f && range <= 1e38f) {
+            // adding 1.5 * 2^23 rounds to a whole number, in the low bits
+            constexpr float kRound = 12582912.0f;
+            const float inv = __frcp_rn(s) * (1.0f + 0x1p-21f);
+            float low = 0.0f;
+            float2 r[8], e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double r = rint(((double)x[i] - (double)lo) / (double)s);
-                code |= (uint32_t)fmin(r, 15.0) << (4 * i);
+                const float2 t = add2(x[i], twice(-lo));
+                r[i] = fma2(t, twice(inv), twice(kRound));
+                const float2 k = add2(r[i], twice(-kRound));
+                e[i] = fma2(k, twice(-s), t);
+                low = fminf(low, fminf(e[i].x, e[i].y));
+                c[i >> 2] += __float_as_uint(r[i].x) * (1u << (8 * (i & 3)));
+                c[i >> 2] += __float_as_uint(r[i].y) * (16u << (8 * (i & 3)));
             }
-    } else {
-        const float inv = 1.0f / s;
+            // less the bits of 1.5 * 2^23 in each of the eight places
+            c[0] -= 0x4b400000u * 0x11111111u;
+            c[1] -= 0x4b400000u * 0x11111111u;
+            const float near = -0.5f * s * (1.0f - 0x1p-21f);
+            if (low <= near) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = (x[i] - lo) * inv;
-            float r = rintf(q);
-            if (fabsf(q - r) > 0.4999f) {
-                const float k = floorf(q);
-                const double e =
-                    ((double)x[i] - (double)lo) - ((double)k + 0.5) * (double)s;
-                const bool up = e > 0.0 || (e == 0.0 && ((int)k & 1));
-                r = up ? k + 1.0f : k;
+                for (int i = 0; i < 8; ++i) {
+                    if (e[i].x <= near)
+                        c[i >> 2] -= too_high(x[i].x, lo, r[i].x - kRound, s) << (8 * (i & 3));
+                    if (e[i].y <= near)
+                        c[i >> 2] -= too_high(x[i].y, lo, r[i].y - kRound, s) << (8 * (i & 3) + 4);
+                }
             }
-            code |= (uint32_t)fminf(r, 15.0f) << (4 * i);
+        } else if (s > 0.0f) {
+            // 1 / s or x - lo may overflow fp32
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double a = rint(((double)x[i].x - (double)lo) / (double)s);
+                const double b = rint(((double)x[i].y - (double)lo) / (double)s);
+                c[i >> 2] |= (uint32_t)fmin(a, 15.0) << (8 * (i & 3));
+                c[i >> 2] |= (uint32_t)fmin(b, 15.0) << (8 * (i & 3) + 4);
+            }
         }
     }
-    return fmaxf(fabsf(lo), fabsf(fmaf(s, 15.0f, lo)));
+    code = make_uint2(c[0], c[1]);
+    return big;
 }
 
 }  // namespace
@@ -145,12 +237,12 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_reset_kernel(Kv4View c, Kv4L
 // Append: its count rows go to the slots from len[b] on, and the last CTA of the grid
 // advances the lengths (every CTA has read them by then).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreadsRows) kv4_rows_kernel(Kv4View c, Kv4Source src,
-                                                                Kv4Lengths lens) {
-    constexpr int LPR = D / 8;                 // lanes a row
+__global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv4Source src,
+                                                                   Kv4Lengths lens) {
+    constexpr int LPR = D / 16;                // lanes a row
     constexpr int RPW = 32 / LPR;              // rows a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rows_cta = (int)(blockDim.x >> 5) * RPW * kUnroll;
+    const int rows_tile = (int)(blockDim.x >> 5) * RPW;
     const int u = blockIdx.y, b = u / c.Hkv, h = u % c.Hkv;
     const bool is_v = blockIdx.z != 0;
     pdl_wait();
@@ -167,50 +259,58 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_rows_kernel(Kv4View c, Kv4So
     } else {
         n = lens.v[b];
     }
-    const int64_t r0 = blockIdx.x * (int64_t)rows_cta;
+    const T* base = reinterpret_cast<const T*>(is_v ? src.v : src.k) + b * src.s_b + h * src.s_h;
+    uint2* codes = reinterpret_cast<uint2*>(is_v ? c.vc : c.kc) + u * c.R * LPR;
+    uint32_t* pars = (is_v ? c.vp : c.kp) + u * c.R * (D / kKv4Group);
+    const int sub = lane % LPR;
+    const int64_t r0 = blockIdx.x * (int64_t)rows_tile * src.tiles;
     float big = 0.0f;
-    if (r0 < n) {
-        const T* base = reinterpret_cast<const T*>(is_v ? src.v : src.k) + b * src.s_b + h * src.s_h;
-        uint32_t* codes = reinterpret_cast<uint32_t*>(is_v ? c.vc : c.kc) + u * c.R * (D / 8);
-        uint32_t* pars = (is_v ? c.vp : c.kp) + u * c.R * (D / kKv4Group);
-        const int sub = lane % LPR;
-        const int64_t r = r0 + (warp * kUnroll) * RPW + lane / LPR;
-        float x[kUnroll][8];
+    Raw<T> raw[kUnroll];
+#pragma unroll 1
+    for (int tile = 0; tile < src.tiles; tile += kUnroll) {
+        const int64_t r = r0 + (int64_t)tile * rows_tile + warp * RPW + lane / LPR;
+        if (r - lane / LPR >= n) break;        // the same for the whole warp
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int64_t row = r + i * RPW;
-            if (row < n) {
-                load8<T>(base + row * src.s_t + sub * 8, x[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
-            }
+            // a row past the last one is read again in its place, and not stored
+            const int64_t row = r + (int64_t)i * rows_tile;
+            load_raw(raw[i], base + (row < n ? row : n - 1) * src.s_t + sub * 16);
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int64_t row = r + i * RPW;
-            uint32_t code, par;
-            big = fmaxf(big, quantize8(x[i], code, par));
+            const int64_t row = r + (int64_t)i * rows_tile;
+            uint2 code;
+            uint32_t par;
+            float2 x[8];
+            float mn, mx;
+            spread(raw[i], x, mn, mx);
+            big = fmaxf(big, quantize16(x, mn, mx, code, par));
             if (row < n) {
                 const int64_t slot = slot0 + row;
-                codes[slot * (D / 8) + sub] = code;
-                if ((sub & 3) == 0) pars[slot * (D / kKv4Group) + (sub >> 2)] = par;
+                codes[slot * LPR + sub] = code;
+                if ((sub & 1) == 0) pars[slot * (D / kKv4Group) + (sub >> 1)] = par;
             }
         }
-        if (!is_v) {
-            for (int i = threadIdx.x; i < rows_cta && r0 + i < n; i += blockDim.x) {
-                const int64_t slot = slot0 + r0 + i;
-                c.pos[u * c.R + slot] = (int32_t)(pos0 + r0 + i);
-                c.w[u * c.R + slot] = 0.0f;
-            }
+    }
+    if (!is_v) {
+        for (int64_t i = r0 + threadIdx.x; i < r0 + rows_tile * src.tiles && i < n; i += blockDim.x) {
+            const int64_t slot = slot0 + i;
+            c.pos[u * c.R + slot] = (int32_t)(pos0 + i);
+            c.w[u * c.R + slot] = 0.0f;
         }
+    }
+    // the CTA's largest value, then one atomic (a maximum does not depend on their order);
+    // a check by every warp made all of them queue at the unit's one word
+    __shared__ float warp_big[kThreadsRows / 32];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-        // the maximum does not depend on the order of the atomics
-        if (lane == 0 && big > 0.0f) {
-            uint32_t* m = (is_v ? c.vmax : c.kmax) + u;
-            if (__float_as_uint(big) > *(volatile uint32_t*)m) atomicMax(m, __float_as_uint(big));
-        }
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+    if (lane == 0) warp_big[warp] = big;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < (int)(blockDim.x >> 5); ++i) big = fmaxf(big, warp_big[i]);
+        uint32_t* m = (is_v ? c.vmax : c.kmax) + u;
+        if (big > 0.0f && __float_as_uint(big) > *(volatile uint32_t*)m)
+            atomicMax(m, __float_as_uint(big));
     }
     if (!src.append) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
@@ -256,11 +356,11 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_read_kernel(Kv4View c, int64
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(is_v ? c.vc : c.kc) + u * c.R * (D / 8);
     const uint32_t* pars = (is_v ? c.vp : c.kp) + u * c.R * (D / kKv4Group);
     const int sub = lane % LPR;
-    const int rows_cta = kThreadsRows / 32 * RPW * kUnroll;
-    const int64_t r = blockIdx.x * (int64_t)rows_cta + (warp * kUnroll) * RPW + lane / LPR;
-    uint32_t code[kUnroll], par[kUnroll];
+    const int rows_cta = kThreadsRows / 32 * RPW * kReadRows;
+    const int64_t r = blockIdx.x * (int64_t)rows_cta + (warp * kReadRows) * RPW + lane / LPR;
+    uint32_t code[kReadRows], par[kReadRows];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         const int64_t slot = start + r + i * RPW;
         code[i] = par[i] = 0;
         if (r + i * RPW < n && slot < L) {
@@ -269,7 +369,7 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_read_kernel(Kv4View c, int64
         }
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         const int64_t row = r + i * RPW;
         if (row >= n) continue;
         const float s = kv4_step(par[i]), lo = kv4_off(par[i]);
@@ -310,13 +410,18 @@ cudaError_t kv4_launch_clear(const Kv4View& c, cudaStream_t s) {
 template <typename T, int D>
 static cudaError_t rows_impl(const Kv4View& c, const Kv4Source& src, const Kv4Lengths& lens,
                              cudaStream_t s) {
-    constexpr int per_warp = 32 / (D / 8) * kUnroll;
+    constexpr int per_warp = 32 / (D / 16);
     const int64_t n = src.n;
+    // a lane takes 8 rows where that still fills the GPU, else 2
+    const int64_t units = 2 * (int64_t)c.B * c.Hkv;
+    Kv4Source sized = src;
+    sized.tiles = n * units >= (int64_t)148 * 8 * (kThreadsRows / 32) * per_warp * kTilesRows
+                      ? kTilesRows : kUnroll;
     int threads = kThreadsRows;
-    while (threads > 32 && (threads / 64) * per_warp >= n) threads /= 2;   // few rows: few warps
-    const int64_t rows_cta = (int64_t)(threads / 32) * per_warp;
+    while (threads > 32 && (int64_t)(threads / 64) * per_warp * sized.tiles >= n) threads /= 2;
+    const int64_t rows_cta = (int64_t)(threads / 32) * per_warp * sized.tiles;
     const dim3 grid((unsigned)((n + rows_cta - 1) / rows_cta), (unsigned)(c.B * c.Hkv), 2);
-    return kv4_launch(kv4_rows_kernel<T, D>, grid, threads, 0, s, c, src, lens);
+    return kv4_launch(kv4_rows_kernel<T, D>, grid, threads, 0, s, c, sized, lens);
 }
 
 #define KV4_DISPATCH(FN, ...)                                                   \
@@ -346,7 +451,7 @@ cudaError_t kv4_launch_append(const Kv4View& c, const Kv4Source& src, int dtype,
 template <typename T, int D>
 static cudaError_t read_impl(const Kv4View& c, int64_t start, int64_t n, void* k, void* v,
                              cudaStream_t s) {
-    constexpr int rows_cta = kThreadsRows / 32 * (32 / (D / 8)) * kUnroll;
+    constexpr int rows_cta = kThreadsRows / 32 * (32 / (D / 8)) * kReadRows;
     const dim3 grid((unsigned)((n + rows_cta - 1) / rows_cta), (unsigned)(c.B * c.Hkv), 2);
     return kv4_launch(kv4_read_kernel<T, D>, grid, kThreadsRows, 0, s, c, start, n, (T*)k, (T*)v);
 }

@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, importing this module fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass, field
 
@@ -403,10 +404,19 @@ class RecsaKV4:
         h = ctypes.c_void_p()
         _check(lib.recsa_kv4_init(ctypes.byref(c), capacity, batch, self.max_queries,
                                   _ptr(self.cache), cb, _ptr(self.workspace), wb,
-                                  self._on(stream), ctypes.byref(h)), "recsa_kv4_init")
+                                  _stream(torch.cuda.current_stream(self.device) if stream is None
+                                          else stream), ctypes.byref(h)), "recsa_kv4_init")
         self.handle = h
         self.info = RecsaKV4InfoC()
         _check(lib.recsa_kv4_info(h, ctypes.byref(self.info)), "recsa_kv4_info")
+        # fixed for the handle's life, so that a call of a few microseconds forms none of it
+        self._dtype = cfg.torch_dtype
+        self._index = self.device.index
+        self._q_shape = (batch, cfg.n_q_heads, cfg.head_dim)
+        rows = (batch, cfg.n_kv_heads, self.info.rows)
+        self._positions = self._table(self.cache, self.info.positions, rows, torch.int32)
+        self._weights = self._table(self.cache, self.info.weights, rows, torch.float32)
+        self._lengths = self._table(self.workspace, self.info.lengths, (batch,), torch.int64)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -415,22 +425,28 @@ class RecsaKV4:
             self.handle = None
 
     def _on(self, stream):
-        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        """The raw stream of a call: the given one, else the current one of the cache's device."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        return stream.cuda_stream
 
     def _rows(self, t: torch.Tensor, shape, name: str):
-        if t.dtype != self.cfg.torch_dtype or t.device != self.device:
-            raise ValueError(f"{name}: {t.dtype} on {t.device}, expected "
-                             f"{self.cfg.torch_dtype} on {self.device}")
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        """The address of a contiguous tensor of this shape, the cache's dtype and device."""
+        if t.dtype != self._dtype or t.device != self.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {self._dtype} on "
+                             f"{self.device}")
+        if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: a contiguous tensor of shape {tuple(shape)} expected, got "
                              f"{tuple(t.shape)} with strides {t.stride()}")
+        return t.data_ptr()
 
     def _counts(self, counts):
-        if counts is not None and (counts.dtype != torch.int32 or counts.device != self.device
-                                   or tuple(counts.shape) != (self.batch,)
-                                   or not counts.is_contiguous()):
+        if counts is None:
+            return None
+        if counts.dtype != torch.int32 or counts.device != self.device or \
+                counts.shape != (self.batch,) or not counts.is_contiguous():
             raise ValueError(f"counts: contiguous int32 [{self.batch}] on {self.device} expected")
-        return _ptr(counts)
+        return counts.data_ptr()
 
     # --- the C-ABI calls -------------------------------------------------------
     def recsa_kv4_build(self, k: torch.Tensor, v: torch.Tensor, lengths, stream=None):
@@ -438,8 +454,8 @@ class RecsaKV4:
         lens = [int(x) for x in lengths]
         c = self.cfg
         for t, name in ((k, "k"), (v, "v")):
-            if t.dtype != c.torch_dtype or t.device != self.device:
-                raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {c.torch_dtype} on "
+            if t.dtype != self._dtype or t.device != self.device:
+                raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {self._dtype} on "
                                  f"{self.device}")
             if t.dim() != 4 or t.shape[:2] != (self.batch, c.n_kv_heads) or \
                     t.shape[3] != c.head_dim or t.stride(3) != 1:
@@ -453,32 +469,29 @@ class RecsaKV4:
         # a dim of one element has no stride that matters: the library checks all three
         st = [s if n > 1 else c.head_dim for s, n in zip(k.stride()[:3], k.shape[:3])]
         strides = (ctypes.c_int64 * 3)(*st)
-        _check(lib.recsa_kv4_build(self.handle, _ptr(k), _ptr(v), strides, arr, self._on(stream)),
-               "recsa_kv4_build")
+        _check(lib.recsa_kv4_build(self.handle, k.data_ptr(), v.data_ptr(), strides, arr,
+                                   self._on(stream)), "recsa_kv4_build")
 
     def recsa_kv4_append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts=None, stream=None):
         n = k_new.shape[2]
         shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
-        self._rows(k_new, shape, "k_new")
-        self._rows(v_new, shape, "v_new")
-        _check(lib.recsa_kv4_append(self.handle, _ptr(k_new), _ptr(v_new), n, self._counts(counts),
+        _check(lib.recsa_kv4_append(self.handle, self._rows(k_new, shape, "k_new"),
+                                    self._rows(v_new, shape, "v_new"), n, self._counts(counts),
                                     self._on(stream)), "recsa_kv4_append")
 
     def recsa_kv4_decode(self, q: torch.Tensor, out: torch.Tensor, accumulate: bool = False,
                          stream=None):
-        shape = (self.batch, self.cfg.n_q_heads, self.cfg.head_dim)
-        self._rows(q, shape, "q")
-        self._rows(out, shape, "out")
-        _check(lib.recsa_kv4_decode(self.handle, _ptr(q), _ptr(out), int(bool(accumulate)),
+        shape = self._q_shape
+        _check(lib.recsa_kv4_decode(self.handle, self._rows(q, shape, "q"),
+                                    self._rows(out, shape, "out"), 1 if accumulate else 0,
                                     self._on(stream)), "recsa_kv4_decode")
 
     def recsa_kv4_prefill_chunk(self, Q: torch.Tensor, O: torch.Tensor, counts=None,
                                 accumulate_rows: int = 0, stream=None):
         n = Q.shape[1]
         shape = (self.batch, n, self.cfg.n_q_heads, self.cfg.head_dim)
-        self._rows(Q, shape, "Q")
-        self._rows(O, shape, "O")
-        _check(lib.recsa_kv4_prefill_chunk(self.handle, _ptr(Q), n, self._counts(counts), _ptr(O),
+        _check(lib.recsa_kv4_prefill_chunk(self.handle, self._rows(Q, shape, "Q"), n,
+                                           self._counts(counts), self._rows(O, shape, "O"),
                                            accumulate_rows, self._on(stream)),
                "recsa_kv4_prefill_chunk")
 
@@ -488,11 +501,9 @@ class RecsaKV4:
 
     def recsa_kv4_read(self, start: int, n: int, k_out=None, v_out=None, stream=None):
         shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is not None:
-                self._rows(t, shape, name)
-        _check(lib.recsa_kv4_read(self.handle, start, n, _ptr(k_out), _ptr(v_out),
-                                  self._on(stream)), "recsa_kv4_read")
+        k = None if k_out is None else self._rows(k_out, shape, "k_out")
+        v = None if v_out is None else self._rows(v_out, shape, "v_out")
+        _check(lib.recsa_kv4_read(self.handle, start, n, k, v, self._on(stream)), "recsa_kv4_read")
 
     def recsa_kv4_get_status(self, stream=None) -> int:
         return lib.recsa_kv4_get_status(self.handle, self._on(stream))
@@ -517,19 +528,17 @@ class RecsaKV4:
         return k, v
 
     def _table(self, buf: torch.Tensor, offset: int, shape, dtype):
-        n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        n = math.prod(shape) * dtype.itemsize
         return buf[offset: offset + n].view(dtype).view(shape)
 
     def positions(self):
         """int32 view [batch][Hkv][rows] of the slots' token positions (0 past the length)."""
-        return self._table(self.cache, self.info.positions,
-                           (self.batch, self.cfg.n_kv_heads, self.info.rows), torch.int32)
+        return self._positions
 
     def weights(self):
         """fp32 view [batch][Hkv][rows] of the accumulated weights (0 past the length)."""
-        return self._table(self.cache, self.info.weights,
-                           (self.batch, self.cfg.n_kv_heads, self.info.rows), torch.float32)
+        return self._weights
 
     def lengths(self):
         """int64 view [batch] of the device-side lengths."""
-        return self._table(self.workspace, self.info.lengths, (self.batch,), torch.int64)
+        return self._lengths
