@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "librecsa.so")
 SOURCES = ["recsa_api.cu", "tree_kernels.cu", "select_attend.cu", "prefill_tc.cu", "noalloc.cu",
            "gated.cu", "offload.cu", "kv4_api.cu", "kv4_rows.cu", "kv4_attend.cu",
-           "kv4_evict.cu"]
+           "kv4_chunk.cu", "kv4_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

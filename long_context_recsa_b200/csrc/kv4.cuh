@@ -53,7 +53,7 @@ struct Kv4Source {
 
 // Scratch of the attention kernels.
 struct Kv4Scratch {
-    float* part;             // [2 * grid][rows a block][D + 2] split-softmax partials
+    float* part;             // [2 * grid][rows a block][D + 2] split-softmax partials (both kernels')
     uint32_t* ucnt;          // [3 * grid] arrivals at the joins of split units (left at 0)
     float* lse;              // [U][rows] log2 of each row's softmax sum
 };
@@ -83,6 +83,10 @@ size_t kv4_attend_part_floats(int D);                   // floats of Kv4Scratch:
 cudaError_t kv4_prepare_attend(int dtype, int D);
 cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s);
+size_t kv4_chunk_part_floats(int D, int rows);          // the same for kv4_launch_chunk
+cudaError_t kv4_prepare_chunk(int D);
+// bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows
+cudaError_t kv4_launch_chunk(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s);
 cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
                                const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s);
 

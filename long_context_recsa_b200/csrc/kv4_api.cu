@@ -20,6 +20,10 @@ struct Kv4Layout {
     size_t o_status, o_done, o_len, o_seen, o_kmax, o_vmax, o_ucnt, o_lse, o_part, o_lists, ws_bytes;
 };
 
+// Rows (chunk rows times heads of a group) of one wave and KV head that kv4_launch_chunk takes:
+// what does not fit the 8 columns of the other kernel's narrowest form, in bf16.
+bool chunk_on_tensor_cores(int dtype, int rows) { return dtype == RECSA_BF16 && rows > 8; }
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -57,7 +61,12 @@ recsa_status kv4_layout(const recsa_config* c, int64_t cap, int B, int Qmax, Kv4
     L->o_vmax = w;   w = up256(w + sizeof(uint32_t) * L->U);
     L->o_ucnt = w;   w = up256(w + sizeof(uint32_t) * kv4_attend_counters());
     L->o_lse = w;    w = up256(w + sizeof(float) * (size_t)Qmax * c->n_q_heads);
-    L->o_part = w;   w = up256(w + sizeof(float) * kv4_attend_part_floats(L->D));
+    size_t part = kv4_attend_part_floats(L->D);
+    if (chunk_on_tensor_cores(c->dtype, Qmax / B * G)) {
+        const size_t p = kv4_chunk_part_floats(L->D, Qmax / B * G);
+        if (p > part) part = p;
+    }
+    L->o_part = w;   w = up256(w + sizeof(float) * part);
     L->o_lists = w;  w = up256(w + sizeof(int32_t) * rows);
     L->ws_bytes = w;
     return RECSA_OK;
@@ -207,6 +216,7 @@ recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t b
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = on.ok ? kv4_prepare_attend(cfg->dtype, L.D) : cudaErrorInvalidDevice;
     if (e == cudaSuccess) e = kv4_prepare_evict(c);
+    if (e == cudaSuccess) e = kv4_prepare_chunk(L.D);
     if (e == cudaSuccess && (!encode_codes(&t->maps.k, c.kc, L.D, L.R, L.U, 32) ||
                              !encode_codes(&t->maps.v, c.vc, L.D, L.R, L.U, 32)))
         e = cudaErrorNotSupported;
@@ -303,7 +313,9 @@ recsa_status recsa_kv4_prefill_chunk(recsa_kv4* t, const void* Q, int32_t n, con
         qv.i0 = i0;
         qv.w = n - i0 < wave ? n - i0 : wave;
         qv.acc_rows = accumulate_rows < n ? accumulate_rows : n;
-        e = kv4_launch_attend(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);
+        e = chunk_on_tensor_cores(t->cfg.dtype, qv.w * t->c.G)
+                ? kv4_launch_chunk(t->c, qv, t->sc, s)
+                : kv4_launch_attend(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);
         // with counts the newest rows may lie in any wave, else in the last ones
         if (e == cudaSuccess && qv.acc_rows > 0 && (counts || i0 + qv.w > n - qv.acc_rows))
             e = kv4_launch_weights(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);

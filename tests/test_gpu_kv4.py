@@ -5,7 +5,13 @@ bounded by S = scale * sum |q| (|lo| + 15 s), so it is off by at most 16 * 2^-24
 probability by twice that (relative), plus 2^-21 for exp2 and the sums.  P' (probability
 times step) is rounded to fp16 (2^-11; fp32 tensors: twice 11 bits, 2^-21) and meets codes of
 at most 8 in magnitude, so an output adds that times 8 s.  The output is rounded to its type:
-half a step, 2^-8 (bf16) or 2^-24 of it."""
+half a step, 2^-8 (bf16) or 2^-24 of it.
+
+bf16 chunks of more than 8 rows a KV head (`tc`): K and V enter the products as fp16, half a
+step is 2^-11 of each value.  A score is then off by at most 2^-11 * scale * sum |q| |K|, and
+S above is at least twice that sum; P and V are each off by 2^-11, so an output by
+2 * 2^-11 * max |V| more.  These errors are independent from token to token and dim to dim,
+so beside that bound the whole output's error, in norm, is within the bf16 rounding's."""
 import numpy as np
 import pytest
 import torch
@@ -60,13 +66,20 @@ def make(R, dtype, d, Hkv, G, lengths, seed=0, cap=None, max_queries=None, extra
     return kv4, units
 
 
-def bound_of(u, q, dtype):
+def on_tensor_cores(dtype, rows):
+    return dtype == "bf16" and rows > 8
+
+
+def bound_of(u, q, dtype, tc=False):
     """(score error, tolerance floor of an output) of one unit and query rows q [G][d]."""
     if len(u.k) == 0:
         return 0.0, 0.0
     big = np.abs(u.k).max(0) * 2 + 1e-30
     S = u.scale * (np.abs(q) @ big).max()
     delta = 16 * 2.0 ** -24 * S
+    if tc:
+        delta += 2.0 ** -12 * S
+        return delta, (2 * delta + 2.0 ** -10) * np.abs(u.v).max()
     g = u.v.reshape(len(u.v), -1, 32)
     step8 = 8.0 / 15.0 * 1.01 * (g.max(-1) - g.min(-1)).max()
     return delta, PROB[dtype] * step8 + (2 * delta + 2.0 ** -21) * np.abs(u.v).max()
@@ -86,11 +99,11 @@ def check_decode(kv4, units, q, out, dtype, G):
             check_rows(out[b, h * G:(h + 1) * G], want, bound_of(u, qs, dtype)[1], dtype, (b, h))
 
 
-def check_weights(kv4, units, dtype, rows, q_all):
+def check_weights(kv4, units, dtype, rows, q_all, tc=False):
     w = np64(kv4.weights())
     for b, row in enumerate(units):
         for h, u in enumerate(row):
-            delta = bound_of(u, q_all[b, h], dtype)[0]
+            delta = bound_of(u, q_all[b, h], dtype, tc)[0]
             err = np.abs(w[b, h, :len(u.w)] - u.w)
             assert (err <= (2 * delta + 2.0 ** -19) * np.abs(u.w) + 1e-30).all(), (b, h, err.max())
             assert (w[b, h, len(u.w):] == 0).all()
@@ -281,7 +294,9 @@ def test_values_of_unequal_magnitude(R):
 @pytest.mark.parametrize("d,Hkv,G,lengths,n,counts,mq", [
     (64, 1, 1, [5], 5, None, None), (128, 2, 4, [40, 33], 3, None, None),
     (128, 1, 8, [100, 9, 64], 9, [9, 0, 4], 5 * 3), (64, 2, 2, [200, 77], 50, [50, 13], 2 * 50),
-    (64, 1, 4, [0, 130], 7, [0, 7], 2 * 7), (128, 1, 2, [150], 150, None, 64), (64, 1, 1, [1], 1, None, 1)])
+    (64, 1, 4, [0, 130], 7, [0, 7], 2 * 7), (128, 1, 2, [150], 150, None, 64), (64, 1, 1, [1], 1, None, 1),
+    (128, 2, 4, [129, 500], 33, None, 2 * 33), (128, 1, 1, [1030], 300, None, 300), (64, 1, 8, [400], 70, None, 40),
+    (64, 2, 1, [128, 127, 9], 9, [9, 0, 5], 3 * 9), (128, 1, 4, [260], 260, None, 260)])
 def test_chunk(R, dtype, d, Hkv, G, lengths, n, counts, mq):
     B = len(lengths)
     kv4, units = make(R, dtype, d, Hkv, G, lengths, max_queries=mq)
@@ -289,7 +304,10 @@ def test_chunk(R, dtype, d, Hkv, G, lengths, n, counts, mq):
     c = None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
     O_ = torch.full((B, n, G * Hkv, d), 5.0, dtype=DT[dtype], device="cuda")
     acc = max(1, n // 3)
+    wave = min(n, (mq or B) // B)
+    tc = on_tensor_cores(dtype, wave * G)
     kv4.recsa_kv4_prefill_chunk(Q.cuda(), O_, c, accumulate_rows=acc)
+    off = size = 0.0
     for b in range(B):
         m = n if counts is None else counts[b]
         assert (O_[b, m:] == 5.0).all()                  # rows behind are left as they were
@@ -299,9 +317,13 @@ def test_chunk(R, dtype, d, Hkv, G, lengths, n, counts, mq):
                 u = units[b][h]
                 qs = np64(Q[b, i, h * G:(h + 1) * G])
                 want = u.attend(qs, at, accumulate=i >= m - acc)
-                check_rows(O_[b, i, h * G:(h + 1) * G], want, bound_of(u, qs, dtype)[1], dtype, (b, i, h))
+                got = O_[b, i, h * G:(h + 1) * G]
+                check_rows(got, want, bound_of(u, qs, dtype, tc)[1], dtype, (b, i, h))
+                off += ((np64(got) - want) ** 2).sum()
+                size += (want ** 2).sum()
+    assert off ** 0.5 <= HALF[dtype] * size ** 0.5 + (0 if dtype == "bf16" else 2.0 ** -20 * size ** 0.5)
     q_all = np64(Q).reshape(B, n, Hkv, G, d).transpose(0, 2, 1, 3, 4).reshape(B, Hkv, -1, d)
-    check_weights(kv4, units, dtype, acc, q_all)
+    check_weights(kv4, units, dtype, acc, q_all, tc)
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK
 
 
@@ -314,6 +336,11 @@ def test_chunk_refuses_more_rows_than_tokens(R):
     assert (O_[0] == 9.0).all() and (O_[1] != 9.0).any()  # the other sequence's rows are right
     want = units[1][0].attend(np64(Q[1, 4]), 19)
     check_rows(O_[1, 4], want, bound_of(units[1][0], np64(Q[1, 4]), "bf16")[1], "bf16", "row")
+    big = R.RecsaKV4(kv4.cfg, 20, 2, max_queries=10)     # the same on the tensor cores
+    big.recsa_kv4_append(rand((2, 1, 3, 64), 2, "bf16").cuda(), rand((2, 1, 3, 64), 3, "bf16").cuda())
+    O_.fill_(9.0)
+    big.recsa_kv4_prefill_chunk(Q, O_)
+    assert big.recsa_kv4_get_status() == R.RECSA_E_DEVICE and (O_ == 9.0).all()
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("bf16", 64)])
@@ -431,7 +458,8 @@ def test_a_bounded_cache_in_use(R, dtype, d, G):
                     u = units[b][h]
                     qs = np64(Q[b, i, h * G:(h + 1) * G])
                     want = u.attend(qs, u.seen - m + i, accumulate=i >= m - acc)
-                    check_rows(out[b, i, h * G:(h + 1) * G], want, bound_of(u, qs, dtype)[1], dtype, (b, i, h))
+                    tc = on_tensor_cores(dtype, min(n, 64) * G)
+                    check_rows(out[b, i, h * G:(h + 1) * G], want, bound_of(u, qs, dtype, tc)[1], dtype, (b, i, h))
 
     def evict():
         # near-equal weights may rank either way: take the library's own weights
