@@ -117,9 +117,10 @@ __device__ __forceinline__ uint32_t centre_hi(uint32_t x) {
     const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&m));
     return *reinterpret_cast<const uint32_t*>(&a);
 }
+// (without .ftz every call is wrapped in the scaling of subnormal results)
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // 2^e for a whole e, clamped to the normal range.

@@ -11,7 +11,7 @@
 // With more than 128 rows the streams are two blocks of rows over the same tokens, else the
 // even and the odd tiles of the same rows, whose results are joined at the end.
 //
-// Eight warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
+// Four warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
 // halves, less 1024 is the code, and one HFMA2 gives lo + s * code, rounded once (2^-12 of
 // the value).  K, V and q are scaled by powers of two into fp16's range (the largest |K|
 // and |V| of a unit are kept by the writes); a bf16 q is exact there.  P is scaled to at most
@@ -35,9 +35,12 @@ namespace {
 
 constexpr int kTok = 128;                 // tokens of a tile
 constexpr int kRowsStream = 128;
-constexpr int kSoftWarps = 8;             // two warpgroups, a stream each
-constexpr int kKWarp0 = 8, kVWarp0 = 12, kMmaWarp = 16;
-constexpr int kChunkThreads = 17 * 32;
+// Warpgroups 0 and 1: softmax, a stream each; 2: codes to fp16; 3: its first warp issues the
+// products.  Registers a thread of each: all 65536 of the launch (512 x 128) are shared out.
+constexpr int kSoftWarps = 8, kCodeWarp0 = 8, kMmaWarp = 12;
+constexpr int kChunkThreads = 512;
+constexpr int kSoftRegs = 184, kCodeRegs = 96, kMmaRegs = 48;
+static_assert(2 * kSoftRegs + kCodeRegs + kMmaRegs == 4 * 128, "more registers than the launch has");
 constexpr int kInfo = 4;                  // tiles whose positions are held (see the ring's use)
 constexpr float kUp = 8.0f;               // P is scaled by 2^8, and stays below 2^14
 constexpr float kGrow = 6.0f;
@@ -194,7 +197,18 @@ __device__ __forceinline__ void ld32(uint32_t t, float (&v)[32]) {
         : "r"(t)
         : "memory");
 }
-__device__ __forceinline__ void ld_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads before it; names the registers, so that none is used earlier.
+__device__ __forceinline__ void ld_done(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+                   "+f"(v[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st32(uint32_t t, const float (&v)[32]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
@@ -225,9 +239,10 @@ __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// (without .ftz every call is wrapped in the scaling of subnormal results)
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float pow2i(int e) {   // 2^e, clamped to the normal range
@@ -257,31 +272,34 @@ __device__ __forceinline__ uint4 values8(uint32_t w, __half2 s, __half2 lo) {
     return v;
 }
 
-// What a thread of the dequantising warps holds of its token's row.
+// What a thread of the converting warps holds of its token's row.
 template <int D> struct TokenRow {
     uint4 codes[D / 32];
     uint32_t par[D / 32];
 };
 template <int D>
+__device__ __forceinline__ void load_pars(uint32_t (&par)[D / 32], const uint32_t* pars, int64_t row) {
+    if constexpr (D == 128) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(pars) + row);
+        par[0] = v.x; par[1] = v.y; par[2] = v.z; par[3] = v.w;
+    } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(pars) + row);
+        par[0] = v.x; par[1] = v.y;
+    }
+}
+template <int D>
 __device__ __forceinline__ void load_token(TokenRow<D>& t, const uint8_t* codes, const uint32_t* pars,
                                            int64_t row, bool there) {
-    constexpr int NG = D / 32;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
+    for (int j = 0; j < D / 32; ++j) {
         t.codes[j] = make_uint4(0, 0, 0, 0);
         t.par[j] = 0;
     }
     if (!there) return;
-    const uint4* p = reinterpret_cast<const uint4*>(codes) + row * NG;
+    const uint4* p = reinterpret_cast<const uint4*>(codes) + row * (D / 32);
 #pragma unroll
-    for (int j = 0; j < NG; ++j) t.codes[j] = __ldg(p + j);
-    if constexpr (NG == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(pars) + row);
-        t.par[0] = v.x; t.par[1] = v.y; t.par[2] = v.z; t.par[3] = v.w;
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(pars) + row);
-        t.par[0] = v.x; t.par[1] = v.y;
-    }
+    for (int j = 0; j < D / 32; ++j) t.codes[j] = __ldg(p + j);
+    load_pars<D>(t.par, pars, row);
 }
 template <int D>
 __device__ __forceinline__ void put_token(unsigned char* tile, const TokenRow<D>& t, int row,
@@ -295,6 +313,23 @@ __device__ __forceinline__ void put_token(unsigned char* tile, const TokenRow<D>
         for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint4*>(tile + chunk_of(row, j * 4 + k)) = values8(w[k], s, lo);
     }
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return y;
 }
 
 // Tiles a CTA takes; two at least, one for each stream.
@@ -320,6 +355,20 @@ struct ChunkBars {
 
 }  // namespace
 
+// What all threads of a CTA know of the unit they work on.
+struct ChunkUnit {
+    int64_t start;            // the unit's first tile in the list
+    int b, h, u;
+    int tiles, tile0, T;      // of the unit; the first that this CTA takes, and how many
+    int row0, row_end, n_b;   // rows of the sequence (chunk row times G + head of the group)
+    int X;                    // products: x = 0, 1, .., of stream x & 1
+};
+
+__device__ __forceinline__ void all_threads() {
+    __syncwarp();
+    asm volatile("bar.sync 0;" ::: "memory");
+}
+
 // part: [2 * grid] of: O [D / 4][RB] float4, m [RB], l [RB].
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, Kv4Query qv,
@@ -330,6 +379,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChunkPlan pl;
+    __shared__ ChunkUnit un;
     __shared__ ChunkBars bars;
     __shared__ __align__(16) int32_t pos_s[kInfo][kTok];
     __shared__ __align__(16) int32_t pos_max[kInfo][4];
@@ -337,12 +387,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     __shared__ __align__(16) uint32_t nan_any[kInfo][4];
     __shared__ float join_m[kRowsStream], join_l[kRowsStream];
     __shared__ uint32_t join_nan[kRowsStream];
-    __shared__ int unit_h, unit_rb;
-    __shared__ int64_t unit_start;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool two_blocks = RB == 256;        // else the streams share their rows
+    const int sh = two_blocks ? 1 : 0;        // tile of product x: x >> sh
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -371,8 +420,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     const uint32_t tmem = tmem_slot;
     const int64_t total = pl.pre[c.B];
     const int64_t quota = chunk_quota(total, gridDim.x);
-    int64_t at = blockIdx.x * quota;
-    const int64_t at_end = at + quota < total ? at + quota : total;
+    const int64_t at0 = blockIdx.x * quota;
+    const int64_t at_end = at0 + quota < total ? at0 + quota : total;
 
     // a wait of this CTA that gave up ends the CTA's work (all waits are bounded)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -381,51 +430,70 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         failed = 1;
         return false;
     };
-
-    // uses of each barrier so far give the parities
-    uint32_t n_tiles = 0, n_x[2] = {0, 0}, n_units = 0;
-
-    int b = 0;
-    while (at < at_end) {
-        while (pl.pre[b + 1] <= at) ++b;
-        if (threadIdx.x == 0) {
-            int h, rb;
-            int64_t start;
-            unit_at(pl, b, at - pl.pre[b], h, rb, start);
-            unit_h = h;
-            unit_rb = rb;
-            unit_start = pl.pre[b] + start;
+    // The units of this CTA, by every role in its own branch: stage() before the rows of Q are
+    // needed, then work().  Uses of the barriers so far give their parities.
+    uint32_t n_tiles = 0, n_units = 0, n_x0 = 0, n_x1 = 0;
+    auto for_units = [&](auto stage, auto work) {
+        int64_t at = at0;
+        int b = 0;
+        while (at < at_end) {
+            if (threadIdx.x == 0) {
+                while (pl.pre[b + 1] <= at) ++b;
+                int h, rb;
+                int64_t start;
+                unit_at(pl, b, at - pl.pre[b], h, rb, start);
+                un.b = b;
+                un.h = h;
+                un.u = b * c.Hkv + h;
+                un.start = start + pl.pre[b];
+                un.tiles = tiles_of(pl, b, rb);
+                un.tile0 = (int)(at - un.start);
+                const int64_t left = at_end - at;
+                un.T = (int)(left < un.tiles - un.tile0 ? left : un.tiles - un.tile0);
+                un.n_b = qv.counts ? qv.counts[b] : qv.n;
+                const int w_end = qv.i0 + qv.w < un.n_b ? qv.i0 + qv.w : un.n_b;
+                un.row0 = qv.i0 * c.G + rb * RB;
+                un.row_end = w_end * c.G;
+                un.X = un.T << sh;
+            }
+            all_threads();
+            stage();
+            all_threads();
+            work();
+            const int X = un.X;
+            at += un.T;
+            n_tiles += un.T;
+            n_x0 += (X + 1) / 2;
+            n_x1 += X / 2;
+            ++n_units;
+            tc_before();
+            all_threads();
+            tc_after();
+            if (failed) break;
         }
-        __syncthreads();
-        const int h = unit_h, rb = unit_rb, u = b * c.Hkv + h;
-        const int64_t start = unit_start;
-        const int tiles = tiles_of(pl, b, rb), tile0 = (int)(at - start);
-        const int T = (int)(at_end - at < tiles - tile0 ? at_end - at : tiles - tile0);
-        const int64_t L = c.len[b], seen = c.seen[b];
-        const int n_b = qv.counts ? qv.counts[b] : qv.n;
-        const int w_end = qv.i0 + qv.w < n_b ? qv.i0 + qv.w : n_b;
-        const int row0 = qv.i0 * c.G + rb * RB, row_end = w_end * c.G;
-        const int ek = exponent_of(__uint_as_float(c.kmax[u])), ev = exponent_of(__uint_as_float(c.vmax[u]));
-        // products of the two streams in turn: x = 0, 1, .. ; x's stream is x & 1
-        const int X = two_blocks ? 2 * T : T;
-        const int sh = two_blocks ? 1 : 0;        // tile of x: x >> sh
+    };
 
-        // ---- Q: the softmax warps stage their rows ----
-        int lim = -1;
-        float rsc = 0.0f;
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // ---- softmax: a thread a row ----
         const int stream = warp >> 2, r = threadIdx.x & 127;
-        const int row = row0 + (two_blocks ? stream * kRowsStream : 0) + r;
-        if (warp < kSoftWarps) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + stream * 128, to = tmem + lanes + 256 + stream * 128;
+        int lim = -1, row = 0;
+        float rsc = 0.0f;
+        auto stage = [&] {
+            // this thread's row of Q, scaled by a power of two to [2^10, 2^11)
+            row = un.row0 + (two_blocks ? stream * kRowsStream : 0) + r;
+            lim = -1;
             unsigned char* qs = smem + Sm::kQ + stream * Sm::kTileBytes;
-            const bool live = row < row_end;
             uint4 raw[D / 8];
             float mx = 0.0f;
-            if (live) {
+            if (row < un.row_end) {
                 const int i = row / c.G, g = row % c.G;
-                lim = (int)(seen - n_b + i);
+                lim = (int)(c.seen[un.b] - un.n_b + i);
                 const uint4* q = reinterpret_cast<const uint4*>(
                     reinterpret_cast<const __nv_bfloat16*>(qv.q) +
-                    (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D);
+                    (((int64_t)un.b * qv.n + i) * c.Hq + un.h * c.G + g) * D);
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(q + k);
             } else {
@@ -440,6 +508,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
                                          fabsf(__uint_as_float(w[e] & 0xffff0000u))));
             }
+            const int ek = exponent_of(__uint_as_float(c.kmax[un.u]));
             const int e0 = exponent_of(mx), eq = e0 < -116 ? -116 : e0;
             const float up = pow2i(10 - eq);
             rsc = fmaxf(fminf(c.scale * 1.4426950408889634f * pow2i(eq - 10 + ek - 13), 3e38f), 1e-38f);
@@ -460,130 +529,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 *reinterpret_cast<uint4*>(qs + chunk_of(r, k)) = y;
             }
             fence_async_smem();
-        }
-        __syncthreads();
-
-        if (warp >= kKWarp0 && warp < kMmaWarp) {
-            // ---- codes to fp16: four warps K, four V, a thread a token ----
-            const bool is_v = warp >= kVWarp0;
-            const int tok = threadIdx.x & 127;
-            const uint8_t* codes = (is_v ? c.vc : c.kc) + u * c.R * (D / 2);
-            const uint32_t* pars = (is_v ? c.vp : c.kp) + u * c.R * NG;
-            const uint32_t* vpars = c.vp + u * c.R * NG;
-            const float scale = pow2i(13 - (is_v ? ev : ek));
-            uint64_t* full = is_v ? bars.v_full : bars.k_full;
-            uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
-            unsigned char* ring = smem + (is_v ? Sm::kV : Sm::kK);
-            TokenRow<D> cur, nxt;
-            int64_t t_row = (int64_t)tile0 * kTok + tok;
-            load_token<D>(nxt, codes, pars, t_row, t_row < L);
-            for (int t = 0; t < T; ++t) {
-                const uint32_t n = n_tiles + t;
-                cur = nxt;
-                const int64_t row_t = (int64_t)(tile0 + t) * kTok + tok;
-                const bool there = row_t < L;
-                int32_t pos = 0x7fffffff;
-                uint32_t vnan = 0;
-                if (!is_v && there) {
-                    pos = __ldg(c.pos + u * c.R + row_t);
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        vnan |= (__ldg(vpars + row_t * NG + j) == kNanPar ? 1u : 0u) << j;
-                }
-                if (t + 1 < T) load_token<D>(nxt, codes, pars, row_t + kTok, row_t + kTok < L);
-                const uint32_t st = n & 1;
-                if (!wait(&empty[st], ((n >> 1) & 1) ^ 1)) break;
-                if (is_v) {
-                    // the rows that see a NaN group learn of it by nan_s; in a product
-                    // it would reach all rows
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        if (cur.par[j] == kNanPar) cur.par[j] = 0;
-                } else {
-                    const int slot = n % kInfo, wq = warp - kKWarp0;
-                    pos_s[slot][tok] = pos;
-                    const int32_t most = __reduce_max_sync(kFull, pos);
-                    const bool any = __any_sync(kFull, vnan != 0);
-                    if (any) {
-#pragma unroll
-                        for (int j = 0; j < NG; ++j) {
-                            const uint32_t m = __ballot_sync(kFull, (vnan >> j) & 1u);
-                            if (lane == 0) nan_s[slot][wq][j] = m;
-                        }
-                    }
-                    if (lane == 0) {
-                        pos_max[slot][wq] = most;
-                        nan_any[slot][wq] = any;
-                    }
-                }
-                put_token<D>(ring + st * Sm::kTileBytes, cur, tok, scale);
-                fence_async_smem();
-                mbar_arrive(&full[st]);
-            }
-        } else if (warp == kMmaWarp) {
-            // ---- products ----
-            if (lane == 0) {
-                constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
-                const uint32_t q0 = smem_u32(smem + Sm::kQ), k0 = smem_u32(smem + Sm::kK),
-                               v0 = smem_u32(smem + Sm::kV);
-                bool ok = true;
-                auto qk = [&](int x) {
-                    const uint32_t n = n_tiles + (x >> sh), st = n & 1;
-                    ok = ok && wait(&bars.k_full[st], (n >> 1) & 1);
-                    if (!ok) return;
-                    tc_after();
-                    const uint32_t qa = q0 + (x & 1) * Sm::kTileBytes, ka = k0 + st * Sm::kTileBytes;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * Sm::kSlab + (k & 3) * 32;
-                        mma_ss(tmem + (x & 1) * 128, sw128(qa + off, 16), sw128(ka + off, 16), id_qk, k > 0);
-                    }
-                    commit(&bars.s_full[x & 1]);
-                    if (!two_blocks || (x & 1)) commit(&bars.k_empty[st]);
-                };
-                qk(0);
-                if (X > 1) qk(1);
-                for (int x = 0; ok && x < X; ++x) {
-                    const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
-                    ok = ok && wait(&bars.v_full[st], (n >> 1) & 1) &&
-                         wait(&bars.p_full[i], (n_x[i] + (x >> 1)) & 1);
-                    if (!ok) break;
-                    tc_after();
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8,
-                               sw128(v0 + st * Sm::kTileBytes + k * 2048, Sm::kSlab), id_pv,
-                               x > 1 || k > 0);
-                    if (!two_blocks || i) commit(&bars.v_empty[st]);
-                    if (x + 2 < X) qk(x + 2);
-                }
-                commit(&bars.o_full);
-                // after a failure: what was issued is done before TMEM is given back
-                if (!ok) mbar_wait_bounded(&bars.o_full, n_units & 1, c.status, kWaitPollsAfterFail);
-            }
-            __syncwarp();
-        }
-        if (warp < kSoftWarps) {
-            // ---- softmax: a thread a row ----
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t ts = tmem + lanes + stream * 128, to = tmem + lanes + 256 + stream * 128;
-            const int mine = (X - stream + 1) / 2;
+        };
+        auto work = [&] {
+            const int X = un.X, mine = (X - stream + 1) / 2;
             const bool some = __any_sync(kFull, lim >= 0);
-            float m = kKv4MinLog2, l = 0.0f;
+            const uint32_t n_x = stream ? n_x1 : n_x0;
+            float m = kKv4MinLog2;
+            float2 l2 = make_float2(0.0f, 0.0f);
             uint32_t nanbits = 0;
             bool ok = true;
             for (int j = 0; j < mine; ++j) {
-                const int x = 2 * j + stream;
-                const uint32_t slot = (n_tiles + (x >> sh)) % kInfo;
-                ok = ok && wait(&bars.s_full[stream], (n_x[stream] + j) & 1);
-                ok = __all_sync(kFull, ok);
+                const uint32_t slot = (n_tiles + ((2 * j + stream) >> sh)) % kInfo;
+                ok = __all_sync(kFull, wait(&bars.s_full[stream], (n_x + j) & 1));
                 if (!ok) break;
                 tc_after();
                 if (some) {
+                    float s[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) ld32(ts + k * 32, s[k]);
                     const int4 pm = *reinterpret_cast<const int4*>(pos_max[slot]);
+                    const uint4 na = *reinterpret_cast<const uint4*>(nan_any[slot]);
                     const int most = max(max(pm.x, pm.y), max(pm.z, pm.w));
                     const bool masked = __any_sync(kFull, most > lim && lim >= 0);
-                    const uint4 na = *reinterpret_cast<const uint4*>(nan_any[slot]);
                     if (na.x | na.y | na.z | na.w) {
                         for (int q = 0; q < 4; ++q) {
                             if (!nan_any[slot][q]) continue;
@@ -593,34 +560,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                                         nanbits |= ((nan_s[slot][q][g] >> e) & 1u) << g;
                         }
                     }
-                    float s[32];
-                    auto load_scores = [&](int k) {
-                        ld32(ts + k * 32, s);
-                        ld_done();
-                        if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) ld_done(s[k]);
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const int4 p = *reinterpret_cast<const int4*>(&pos_s[slot][k * 32 + e]);
-                                if (p.x > lim) s[e] = -INFINITY;
-                                if (p.y > lim) s[e + 1] = -INFINITY;
-                                if (p.z > lim) s[e + 2] = -INFINITY;
-                                if (p.w > lim) s[e + 3] = -INFINITY;
+                                if (p.x > lim) s[k][e] = -INFINITY;
+                                if (p.y > lim) s[k][e + 1] = -INFINITY;
+                                if (p.z > lim) s[k][e + 2] = -INFINITY;
+                                if (p.w > lim) s[k][e + 3] = -INFINITY;
                             }
-                        }
-                    };
-                    float mx = -INFINITY;
+                    }
+                    float mx4[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        load_scores(k);
+                        mx4[k] = fmaxf(s[k][0], s[k][1]);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(s[e], s[e + 1]));
+                        for (int e = 2; e < 32; e += 2) mx4[k] = fmaxf(mx4[k], fmaxf(s[k][e], s[k][e + 1]));
                     }
-                    mx *= rsc;
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * rsc;
                     if (__any_sync(kFull, mx > m + kGrow)) {
                         const float mn = mx > m + kGrow ? mx : m;
                         const float f = ex2(m - mn);
                         m = mn;
-                        l *= f;
+                        l2.x *= f;
+                        l2.y *= f;
                         if (j > 0) {
                             // the products before S are done (one thread issued both, and
                             // the barrier stands for all it had issued)
@@ -628,27 +595,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                             for (int k = 0; k < D; k += 32) {
                                 float o[32];
                                 ld32(to + k, o);
-                                ld_done();
+                                ld_done(o);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) o[e] *= f;
                                 st32(to + k, o);
                             }
                         }
                     }
-                    const float shift = kUp - m;
+                    const float2 f2 = make_float2(rsc, rsc), shift = make_float2(kUp - m, kUp - m);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        load_scores(k);
                         uint32_t p[16];
-                        float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float a = ex2(fmaf(s[e], rsc, shift)), z = ex2(fmaf(s[e + 1], rsc, shift));
-                            l0 += a;
-                            l1 += z;
-                            p[e >> 1] = as_u(__floats2half2_rn(a, z));
+                            float2 a = fma2(make_float2(s[k][e], s[k][e + 1]), f2, shift);
+                            a.x = ex2(a.x);
+                            a.y = ex2(a.y);
+                            l2 = add2(l2, a);
+                            p[e >> 1] = as_u(__floats2half2_rn(a.x, a.y));
                         }
-                        l += l0 + l1;
                         st16(ts + k * 16, p);
                     }
                     st_done();
@@ -657,10 +622,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 mbar_arrive(&bars.p_full[stream]);
             }
             // ---- results ----
+            float l = l2.x + l2.y;
             ok = __all_sync(kFull, ok && wait(&bars.o_full, n_units & 1));
             tc_after();
-            const int64_t cta0 = start / quota, cta1 = (start + tiles - 1) / quota;
+            const int64_t cta0 = un.start / quota, cta1 = (un.start + un.tiles - 1) / quota;
             const bool whole = cta0 == cta1;
+            const int ev = exponent_of(__uint_as_float(c.vmax[un.u]));
             float f0 = 1.0f, f1 = 0.0f;
             float4* other = reinterpret_cast<float4*>(smem + Sm::kK);   // [D / 4][128]: K is done
             if (!two_blocks) {
@@ -674,7 +641,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                         for (int k = 0; k < D; k += 32) {
                             float o[32];
                             ld32(to + k, o);
-                            ld_done();
+                            ld_done(o);
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
                                 other[(k + e) / 4 * 128 + r] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -692,18 +659,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 }
             }
             if ((two_blocks || stream == 0) && some && ok) {
-                const bool live = row < row_end;
-                const int i = row / c.G, g = row % c.G, rr = row - row0;
+                const bool live = row < un.row_end;
+                const int i = row / c.G, g = row % c.G, rr = row - un.row0;
                 const bool any = l > 0.0f || l != l;
                 const float inv = any ? pow2i(ev - 13) / l : 0.0f;
-                float* part = sc.part + (size_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * RB * (D + 2);
+                float* part = sc.part + (size_t)(2 * blockIdx.x + (un.tile0 == 0 ? 1 : 0)) * RB * (D + 2);
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(qv.out) +
-                                     (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D;
+                                     (((int64_t)un.b * qv.n + i) * c.Hq + un.h * c.G + g) * D;
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     ld32(to + k, o);
-                    ld_done();
+                    ld_done(o);
                     if (f1 != 0.0f) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -734,26 +701,142 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     }
                 }
                 if (live && whole) {
-                    sc.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] =
+                    sc.lse[(int64_t)un.u * qv.w * c.G + row - qv.i0 * c.G] =
                         any ? m - kUp + log2f(l) : INFINITY;
                 } else if (live) {
                     part[(size_t)RB * D + rr] = m;
                     part[(size_t)RB * D + RB + rr] = l;
                 }
             }
-        }
-        at += T;
-        n_tiles += T;
-        n_x[0] += (X + 1) / 2;
-        n_x[1] += X / 2;
-        ++n_units;
-        tc_before();
-        __syncthreads();
-        tc_after();
-        if (failed) break;
+        };
+        for_units(stage, work);
+    } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
+        // ---- codes to fp16: a thread a token; K of the next tile, then V of this one ----
+        const int tok = threadIdx.x & 127, wq = warp - kCodeWarp0;
+        auto work = [&] {
+            const int u = un.u, T = un.T;
+            const int64_t L = c.len[un.b], row0 = (int64_t)un.tile0 * kTok + tok;
+            const float ks = pow2i(13 - exponent_of(__uint_as_float(c.kmax[u])));
+            const float vs = pow2i(13 - exponent_of(__uint_as_float(c.vmax[u])));
+            const uint8_t *kc = c.kc + u * c.R * (D / 2), *vc = c.vc + u * c.R * (D / 2);
+            const uint32_t *kp = c.kp + u * c.R * NG, *vp = c.vp + u * c.R * NG;
+            const int32_t* pos = c.pos + u * c.R;
+            TokenRow<D> kr, vr;
+            uint32_t vpar[NG];
+            int32_t p = 0;
+            auto load_k = [&](int t) {
+                const int64_t row = row0 + (int64_t)t * kTok;
+                load_token<D>(kr, kc, kp, row, row < L);
+                p = 0x7fffffff;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) vpar[j] = 0;
+                if (row < L) {
+                    p = __ldg(pos + row);
+                    load_pars<D>(vpar, vp, row);
+                }
+            };
+            auto put_k = [&](int t) {
+                const uint32_t n = n_tiles + t, st = n & 1, slot = n % kInfo;
+                if (!wait(&bars.k_empty[st], ((n >> 1) & 1) ^ 1)) return false;
+                pos_s[slot][tok] = p;
+                const int32_t most = __reduce_max_sync(kFull, p);
+                uint32_t bad = 0;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) bad |= (vpar[j] == kNanPar ? 1u : 0u) << j;
+                const bool any = __any_sync(kFull, bad != 0);
+                if (any) {
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        const uint32_t mask = __ballot_sync(kFull, (bad >> j) & 1u);
+                        if (lane == 0) nan_s[slot][wq][j] = mask;
+                    }
+                }
+                if (lane == 0) {
+                    pos_max[slot][wq] = most;
+                    nan_any[slot][wq] = any;
+                }
+                put_token<D>(smem + Sm::kK + st * Sm::kTileBytes, kr, tok, ks);
+                fence_async_smem();
+                mbar_arrive(&bars.k_full[st]);
+                return true;
+            };
+            load_k(0);
+            load_token<D>(vr, vc, vp, row0, row0 < L);
+            bool ok = put_k(0);
+            if (T > 1) load_k(1);
+            for (int t = 0; ok && t < T; ++t) {
+                if (t + 1 < T) {
+                    if (!put_k(t + 1)) break;
+                    if (t + 2 < T) load_k(t + 2);
+                }
+                // the rows that see a NaN group learn of it by nan_s; in a product it
+                // would reach all rows
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    if (vr.par[j] == kNanPar) vr.par[j] = 0;
+                const uint32_t n = n_tiles + t, st = n & 1;
+                if (!wait(&bars.v_empty[st], ((n >> 1) & 1) ^ 1)) break;
+                put_token<D>(smem + Sm::kV + st * Sm::kTileBytes, vr, tok, vs);
+                fence_async_smem();
+                mbar_arrive(&bars.v_full[st]);
+                const int64_t row = row0 + (int64_t)(t + 1) * kTok;
+                if (t + 1 < T) load_token<D>(vr, vc, vp, row, row < L);
+            }
+            __syncwarp();
+        };
+        for_units([] {}, work);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        // ---- products ----
+        const uint64_t q0 = sw128(smem_u32(smem + Sm::kQ), 16), k0 = sw128(smem_u32(smem + Sm::kK), 16),
+                       v0 = sw128(smem_u32(smem + Sm::kV), Sm::kSlab);
+        constexpr uint32_t kTile16 = Sm::kTileBytes / 16;   // descriptors count 16 bytes
+        auto work = [&] {
+            if (warp != kMmaWarp || lane != 0) return;
+            constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
+            const int X = un.X;
+            bool ok = true;
+            auto qk = [&](int x) {
+                const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
+                ok = ok && wait(&bars.k_full[st], (n >> 1) & 1);
+                if (!ok) return;
+                tc_after();
+                const uint64_t qa = q0 + i * kTile16, ka = k0 + st * kTile16;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    constexpr int slab16 = Sm::kSlab / 16;
+                    const int off = (k >> 2) * slab16 + (k & 3) * 2;
+                    mma_ss(tmem + i * 128, qa + off, ka + off, id_qk, k > 0);
+                }
+                commit(&bars.s_full[i]);
+                if (!two_blocks || i) commit(&bars.k_empty[st]);
+            };
+            qk(0);
+            if (X > 1) qk(1);
+            for (int x = 0; ok && x < X; ++x) {
+                const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
+                ok = wait(&bars.v_full[st], (n >> 1) & 1) &&
+                     wait(&bars.p_full[i], ((i ? n_x1 : n_x0) + (x >> 1)) & 1);
+                if (!ok) break;
+                tc_after();
+                const uint64_t va = v0 + st * kTile16;
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                    mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, va + k * 128, id_pv,
+                           x > 1 || k > 0);
+                if (!two_blocks || i) commit(&bars.v_empty[st]);
+                if (x + 2 < X) qk(x + 2);
+            }
+            commit(&bars.o_full);
+            // after a failure: what was issued is done before TMEM is given back
+            if (!ok) mbar_wait_bounded(&bars.o_full, n_units & 1, c.status, kWaitPollsAfterFail);
+        };
+        for_units([] {}, work);
+        __syncwarp();
+        if (warp == kMmaWarp)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    if (warp == kMmaWarp)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // Joins the parts of the units that were cut.  Grid: x = 32 rows, y = unit; a lane a row, a
