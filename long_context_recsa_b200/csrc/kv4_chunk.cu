@@ -11,7 +11,7 @@
 // With more than 128 rows the streams are two blocks of rows over the same tokens, else the
 // even and the odd tiles of the same rows, whose results are joined at the end.
 //
-// Four warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
+// Eight warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
 // halves, less 1024 is the code, and one HFMA2 gives lo + s * code, rounded once (2^-12 of
 // the value).  K, V and q are scaled by powers of two into fp16's range (the largest |K|
 // and |V| of a unit are kept by the writes); a bf16 q is exact there.  P is scaled to at most
@@ -35,13 +35,12 @@ namespace {
 
 constexpr int kTok = 128;                 // tokens of a tile
 constexpr int kRowsStream = 128;
-// Warpgroups 0 and 1: softmax, a stream each; 2: codes to fp16; 3: its first warp issues the
-// products.  Registers a thread of each: all 65536 of the launch (512 x 128) are shared out.
-constexpr int kSoftWarps = 8, kCodeWarp0 = 8, kMmaWarp = 12;
-constexpr int kChunkThreads = 512;
-constexpr int kSoftRegs = 184, kCodeRegs = 96, kMmaRegs = 48;
-static_assert(2 * kSoftRegs + kCodeRegs + kMmaRegs == 4 * 128, "more registers than the launch has");
+// Warpgroups 0 and 1: softmax, a stream each; 2 and 3: codes of K and of V to fp16; the last
+// warp issues the products.
+constexpr int kSoftWarps = 8, kCodeWarp0 = 8, kMmaWarp = 16;
+constexpr int kChunkThreads = 17 * 32;
 constexpr int kInfo = 4;                  // tiles whose positions are held (see the ring's use)
+constexpr uint32_t kNanPar = 0x7fc00000u;   // lo = NaN, s = 0
 constexpr float kUp = 8.0f;               // P is scaled by 2^8, and stays below 2^14
 constexpr float kGrow = 6.0f;
 
@@ -52,7 +51,15 @@ struct ChunkSmem {
     static constexpr int kQ = 0;                        // [2 streams]
     static constexpr int kK = 2 * kTileBytes;           // [2 stages]
     static constexpr int kV = 4 * kTileBytes;           // [2 stages]
-    static constexpr int kBytes = 6 * kTileBytes + 1024;
+    static constexpr int kRaw = 6 * kTileBytes;         // a tile of the cache as it lies there
+    // of the raw tile: codes and parameters of K, V's parameters and positions (for the
+    // softmax), codes and parameters of V
+    static constexpr int kCodes = kTok * D / 2, kPars = kTok * D / 8;
+    static constexpr int kRawKp = kCodes, kRawVp = kCodes + kPars, kRawPos = kCodes + 2 * kPars;
+    static constexpr int kRawV = kRawPos + kTok * 4;
+    static constexpr int kRawBytes = kRawV + kCodes + kPars;
+    static constexpr int kBytes = kRaw + kRawBytes + 1024;
+    static_assert(kRawBytes <= kTileBytes, "the second raw tile lies over the second Q");
 };
 
 // The list of tiles: sequence b has nrb[b] blocks of RB rows a KV head; block j sees
@@ -145,6 +152,9 @@ __device__ __forceinline__ void unit_at(const ChunkPlan& p, int b, int64_t in_b,
     start = h * per_h + tiles_before(p, b, lo);
 }
 
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
 // ---- tcgen05 ------------------------------------------------------------------------
 __device__ __forceinline__ void tc_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -232,11 +242,35 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t (&u)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// When the running maximum moves: the row's sums so far, by f <= 1.
+template <int D>
+__device__ __noinline__ void rescale_o(uint32_t t, float f) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        float o[32];
+        ld32(t + k, o);
+        ld_done(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= f;
+        st32(t + k, o);
+    }
+    st_done();
 }
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return y;
 }
 
 // (without .ftz every call is wrapped in the scaling of subnormal results)
@@ -245,6 +279,73 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// ---- softmax of 32 scores of a row ----
+__device__ __forceinline__ float most_of(const float (&s)[32]) {
+    float x = fmaxf(s[0], s[1]), y = fmaxf(s[2], s[3]);
+#pragma unroll
+    for (int e = 4; e < 32; e += 4) {
+        x = fmaxf(x, fmaxf(s[e], s[e + 1]));
+        y = fmaxf(y, fmaxf(s[e + 2], s[e + 3]));
+    }
+    return fmaxf(x, y);
+}
+// Scores of tokens behind position lim become -infinity, in TMEM.  (Not inlined: the few
+// tiles that need it must not lengthen the loop.  The roles' loops run side by side, and when
+// everything was unrolled the SM's instruction cache missed at 64% of the next level's rate.)
+__device__ __noinline__ void hide_scores(uint32_t t, const int32_t* pos, int lim) {
+#pragma unroll 1
+    for (int k = 0; k < kTok; k += 32) {
+        float s[32];
+        ld32(t + k, s);
+        ld_done(s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const int4 p = *reinterpret_cast<const int4*>(pos + k + e);
+            if (p.x > lim) s[e] = -INFINITY;
+            if (p.y > lim) s[e + 1] = -INFINITY;
+            if (p.z > lim) s[e + 2] = -INFINITY;
+            if (p.w > lim) s[e + 3] = -INFINITY;
+        }
+        st32(t + k, s);
+    }
+    st_done();
+}
+// P = 2^(s * scale + shift) as fp16 to TMEM; its sum in fp32 to l2.
+__device__ __forceinline__ void put_p(uint32_t t, const float (&s)[32], float scale, float shift,
+                                      float2& l2) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float2 a = fma2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(shift, shift));
+        a.x = ex2(a.x);
+        a.y = ex2(a.y);
+        l2 = add2(l2, a);
+        p[e >> 1] = as_u(__floats2half2_rn(a.x, a.y));
+    }
+    st16(t, p);
+}
+// Groups of dims in which a token that the row sees holds NaN.
+template <int NG>
+__device__ __noinline__ uint32_t nan_groups(const int32_t* pos, const uint32_t* any,
+                                            const uint32_t (*bits)[4], int lim) {
+    uint32_t out = 0;
+    for (int q = 0; q < 4; ++q) {
+        if (!any[q]) continue;
+        for (int e = 0; e < 32; ++e)
+            if (pos[q * 32 + e] <= lim)
+                for (int g = 0; g < NG; ++g) out |= ((bits[q][g] >> e) & 1u) << g;
+    }
+    return out;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ float pow2i(int e) {   // 2^e, clamped to the normal range
     e = e < -126 ? -126 : e > 127 ? 127 : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
@@ -252,8 +353,6 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, clamped to the normal 
 __device__ __forceinline__ int exponent_of(float x) {
     return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
 }
-__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
 // Place of a 16-byte chunk (8 dims) of a row: slabs of 64 dims, swizzled.
 __device__ __forceinline__ uint32_t chunk_of(int row, int ch) {
@@ -272,64 +371,32 @@ __device__ __forceinline__ uint4 values8(uint32_t w, __half2 s, __half2 lo) {
     return v;
 }
 
-// What a thread of the converting warps holds of its token's row.
-template <int D> struct TokenRow {
-    uint4 codes[D / 32];
-    uint32_t par[D / 32];
-};
+// A raw tile to fp16 values, by 128 threads: a lane takes a group of 32 dims (16 bytes of
+// codes), a warp 32 neighbouring groups, and the upper groups go through their words in
+// another order, so that eight lanes' stores lie in eight different bank groups.  Rows at or
+// past `rows` become 0, and with `drop` groups of NaN too.
 template <int D>
-__device__ __forceinline__ void load_pars(uint32_t (&par)[D / 32], const uint32_t* pars, int64_t row) {
-    if constexpr (D == 128) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(pars) + row);
-        par[0] = v.x; par[1] = v.y; par[2] = v.z; par[3] = v.w;
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(pars) + row);
-        par[0] = v.x; par[1] = v.y;
+__device__ __forceinline__ void convert(unsigned char* tile, const unsigned char* codes,
+                                        const unsigned char* pars, int tid, int rows, float scale,
+                                        bool drop) {
+    constexpr int NG = D / 32;
+#pragma unroll 1
+    for (int i = tid; i < kTok * NG; i += 128) {
+        const int row = i / NG, g = i % NG;
+        const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 16);
+        uint32_t par = *reinterpret_cast<const uint32_t*>(pars + i * 4);
+        if (row >= rows || (drop && par == kNanPar)) par = 0;
+        const __half2 s = __float2half2_rn(kv4_step(par) * scale);
+        const __half2 lo = __float2half2_rn(kv4_off(par) * scale);
+        const bool swap = (g & 2) != 0;
+        const uint32_t w[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+        const int first = g * 4 + (swap ? 2 : 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int ch = (first & ~3) | ((first + k) & 3);
+            *reinterpret_cast<uint4*>(tile + chunk_of(row, ch)) = values8(w[k], s, lo);
+        }
     }
-}
-template <int D>
-__device__ __forceinline__ void load_token(TokenRow<D>& t, const uint8_t* codes, const uint32_t* pars,
-                                           int64_t row, bool there) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        t.codes[j] = make_uint4(0, 0, 0, 0);
-        t.par[j] = 0;
-    }
-    if (!there) return;
-    const uint4* p = reinterpret_cast<const uint4*>(codes) + row * (D / 32);
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) t.codes[j] = __ldg(p + j);
-    load_pars<D>(t.par, pars, row);
-}
-template <int D>
-__device__ __forceinline__ void put_token(unsigned char* tile, const TokenRow<D>& t, int row,
-                                          float scale) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        const __half2 s = __float2half2_rn(kv4_step(t.par[j]) * scale);
-        const __half2 lo = __float2half2_rn(kv4_off(t.par[j]) * scale);
-        const uint32_t w[4] = {t.codes[j].x, t.codes[j].y, t.codes[j].z, t.codes[j].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(tile + chunk_of(row, j * 4 + k)) = values8(w[k], s, lo);
-    }
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-          "l"(reinterpret_cast<uint64_t&>(c)));
-    return y;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 y;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-    return y;
 }
 
 // Tiles a CTA takes; two at least, one for each stream.
@@ -347,10 +414,9 @@ __device__ __forceinline__ uint4 out8(const float* o, float inv) {
     return *reinterpret_cast<const uint4*>(a);
 }
 
-constexpr uint32_t kNanPar = 0x7fc00000u;   // lo = NaN, s = 0
 
 struct ChunkBars {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full;
+    uint64_t raw_full[2][2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full;
 };
 
 }  // namespace
@@ -395,6 +461,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.raw_full[0][i], 1);
+            mbar_init(&bars.raw_full[1][i], 1);
             mbar_init(&bars.k_full[i], 128);
             mbar_init(&bars.k_empty[i], 1);
             mbar_init(&bars.v_full[i], 128);
@@ -474,7 +542,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     };
 
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ---- softmax: a thread a row ----
         const int stream = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -486,35 +553,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             row = un.row0 + (two_blocks ? stream * kRowsStream : 0) + r;
             lim = -1;
             unsigned char* qs = smem + Sm::kQ + stream * Sm::kTileBytes;
-            uint4 raw[D / 8];
+            const uint4* q = nullptr;    // read twice: the row need not fit the registers
             float mx = 0.0f;
             if (row < un.row_end) {
                 const int i = row / c.G, g = row % c.G;
                 lim = (int)(c.seen[un.b] - un.n_b + i);
-                const uint4* q = reinterpret_cast<const uint4*>(
+                q = reinterpret_cast<const uint4*>(
                     reinterpret_cast<const __nv_bfloat16*>(qv.q) +
                     (((int64_t)un.b * qv.n + i) * c.Hq + un.h * c.G + g) * D);
+#pragma unroll 4
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 v = __ldg(q + k);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(q + k);
-            } else {
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) raw[k] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                                         fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                    for (int e = 0; e < 4; ++e)
+                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                                             fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                }
             }
             const int ek = exponent_of(__uint_as_float(c.kmax[un.u]));
             const int e0 = exponent_of(mx), eq = e0 < -116 ? -116 : e0;
             const float up = pow2i(10 - eq);
             rsc = fmaxf(fminf(c.scale * 1.4426950408889634f * pow2i(eq - 10 + ek - 13), 3e38f), 1e-38f);
-#pragma unroll
+#pragma unroll 4
             for (int k = 0; k < D / 8; ++k) {
-                const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (q != nullptr) v = __ldg(q + k);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -526,7 +591,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 y.y = as_u(__floats2half2_rn(x[1], x[5]));
                 y.z = as_u(__floats2half2_rn(x[2], x[6]));
                 y.w = as_u(__floats2half2_rn(x[3], x[7]));
-                *reinterpret_cast<uint4*>(qs + chunk_of(r, k)) = y;
+                if (two_blocks || stream == 0) *reinterpret_cast<uint4*>(qs + chunk_of(r, k)) = y;
             }
             fence_async_smem();
         };
@@ -544,77 +609,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 if (!ok) break;
                 tc_after();
                 if (some) {
-                    float s[4][32];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ld32(ts + k * 32, s[k]);
                     const int4 pm = *reinterpret_cast<const int4*>(pos_max[slot]);
                     const uint4 na = *reinterpret_cast<const uint4*>(nan_any[slot]);
                     const int most = max(max(pm.x, pm.y), max(pm.z, pm.w));
-                    const bool masked = __any_sync(kFull, most > lim && lim >= 0);
-                    if (na.x | na.y | na.z | na.w) {
-                        for (int q = 0; q < 4; ++q) {
-                            if (!nan_any[slot][q]) continue;
-                            for (int e = 0; e < 32; ++e)
-                                if (pos_s[slot][q * 32 + e] <= lim)
-                                    for (int g = 0; g < NG; ++g)
-                                        nanbits |= ((nan_s[slot][q][g] >> e) & 1u) << g;
-                        }
+                    if (__any_sync(kFull, most > lim && lim >= 0)) hide_scores(ts, pos_s[slot], lim);
+                    if (na.x | na.y | na.z | na.w)
+                        nanbits |= nan_groups<NG>(pos_s[slot], nan_any[slot], nan_s[slot], lim);
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int k = 0; k < kTok; k += 64) {
+                        float a[32], z[32];
+                        ld32(ts + k, a);
+                        ld32(ts + k + 32, z);
+                        ld_done(a);
+                        ld_done(z);
+                        mx = fmaxf(mx, fmaxf(most_of(a), most_of(z)));
                     }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ld_done(s[k]);
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const int4 p = *reinterpret_cast<const int4*>(&pos_s[slot][k * 32 + e]);
-                                if (p.x > lim) s[k][e] = -INFINITY;
-                                if (p.y > lim) s[k][e + 1] = -INFINITY;
-                                if (p.z > lim) s[k][e + 2] = -INFINITY;
-                                if (p.w > lim) s[k][e + 3] = -INFINITY;
-                            }
-                    }
-                    float mx4[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        mx4[k] = fmaxf(s[k][0], s[k][1]);
-#pragma unroll
-                        for (int e = 2; e < 32; e += 2) mx4[k] = fmaxf(mx4[k], fmaxf(s[k][e], s[k][e + 1]));
-                    }
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * rsc;
+                    mx *= rsc;
                     if (__any_sync(kFull, mx > m + kGrow)) {
                         const float mn = mx > m + kGrow ? mx : m;
                         const float f = ex2(m - mn);
                         m = mn;
                         l2.x *= f;
                         l2.y *= f;
-                        if (j > 0) {
-                            // the products before S are done (one thread issued both, and
-                            // the barrier stands for all it had issued)
-#pragma unroll 1
-                            for (int k = 0; k < D; k += 32) {
-                                float o[32];
-                                ld32(to + k, o);
-                                ld_done(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= f;
-                                st32(to + k, o);
-                            }
-                        }
+                        // the products before S are done (one thread issued both, and the
+                        // barrier stands for all it had issued)
+                        if (j > 0) rescale_o<D>(to, f);
                     }
-                    const float2 f2 = make_float2(rsc, rsc), shift = make_float2(kUp - m, kUp - m);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 a = fma2(make_float2(s[k][e], s[k][e + 1]), f2, shift);
-                            a.x = ex2(a.x);
-                            a.y = ex2(a.y);
-                            l2 = add2(l2, a);
-                            p[e >> 1] = as_u(__floats2half2_rn(a.x, a.y));
-                        }
-                        st16(ts + k * 16, p);
+#pragma unroll 1
+                    for (int k = 0; k < kTok; k += 64) {
+                        float a[32], z[32];
+                        ld32(ts + k, a);
+                        ld32(ts + k + 32, z);
+                        ld_done(a);
+                        ld_done(z);
+                        put_p(ts + k / 2, a, rsc, kUp - m, l2);
+                        put_p(ts + k / 2 + 16, z, rsc, kUp - m, l2);
                     }
                     st_done();
                 }
@@ -711,89 +741,98 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         };
         for_units(stage, work);
     } else if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
-        // ---- codes to fp16: a thread a token; K of the next tile, then V of this one ----
-        const int tok = threadIdx.x & 127, wq = warp - kCodeWarp0;
+        // ---- codes to fp16: one warpgroup K and what the softmax needs, one V ----
+        const int tid = threadIdx.x & 127, is_v = (warp - kCodeWarp0) >> 2, wq = warp & 3;
+        // raw tiles on their way: the second lies where two blocks have their second Q
+        const int deep = two_blocks ? 1 : 2;
+        auto raw_at = [&](uint32_t n) {
+            return smem + (deep == 2 && (n & 1) ? Sm::kQ + Sm::kTileBytes : Sm::kRaw);
+        };
         auto work = [&] {
-            const int u = un.u, T = un.T;
-            const int64_t L = c.len[un.b], row0 = (int64_t)un.tile0 * kTok + tok;
-            const float ks = pow2i(13 - exponent_of(__uint_as_float(c.kmax[u])));
-            const float vs = pow2i(13 - exponent_of(__uint_as_float(c.vmax[u])));
-            const uint8_t *kc = c.kc + u * c.R * (D / 2), *vc = c.vc + u * c.R * (D / 2);
-            const uint32_t *kp = c.kp + u * c.R * NG, *vp = c.vp + u * c.R * NG;
-            const int32_t* pos = c.pos + u * c.R;
-            TokenRow<D> kr, vr;
-            uint32_t vpar[NG];
-            int32_t p = 0;
-            auto load_k = [&](int t) {
-                const int64_t row = row0 + (int64_t)t * kTok;
-                load_token<D>(kr, kc, kp, row, row < L);
-                p = 0x7fffffff;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) vpar[j] = 0;
-                if (row < L) {
-                    p = __ldg(pos + row);
-                    load_pars<D>(vpar, vp, row);
+            const int u = un.u, T = un.T, tile0 = un.tile0;
+            const int64_t L = c.len[un.b];
+            const float scale = pow2i(13 - exponent_of(__uint_as_float((is_v ? c.vmax : c.kmax)[u])));
+            auto fetch = [&](int t) {
+                const uint32_t n = n_tiles + t;
+                const int64_t row = u * c.R + (int64_t)(tile0 + t) * kTok;
+                unsigned char* raw = raw_at(n);
+                uint64_t* bar = &bars.raw_full[is_v][n & (deep - 1)];
+                if (is_v) {
+                    mbar_expect_tx(bar, Sm::kCodes + Sm::kPars);
+                    bulk_g2s(raw + Sm::kRawV, c.vc + row * (D / 2), Sm::kCodes, bar);
+                    bulk_g2s(raw + Sm::kRawV + Sm::kCodes, c.vp + row * NG, Sm::kPars, bar);
+                } else {
+                    mbar_expect_tx(bar, Sm::kCodes + 2 * Sm::kPars + kTok * 4);
+                    bulk_g2s(raw, c.kc + row * (D / 2), Sm::kCodes, bar);
+                    bulk_g2s(raw + Sm::kRawKp, c.kp + row * NG, Sm::kPars, bar);
+                    bulk_g2s(raw + Sm::kRawVp, c.vp + row * NG, Sm::kPars, bar);
+                    bulk_g2s(raw + Sm::kRawPos, c.pos + row, kTok * 4, bar);
                 }
             };
-            auto put_k = [&](int t) {
-                const uint32_t n = n_tiles + t, st = n & 1, slot = n % kInfo;
-                if (!wait(&bars.k_empty[st], ((n >> 1) & 1) ^ 1)) return false;
-                pos_s[slot][tok] = p;
-                const int32_t most = __reduce_max_sync(kFull, p);
-                uint32_t bad = 0;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) bad |= (vpar[j] == kNanPar ? 1u : 0u) << j;
-                const bool any = __any_sync(kFull, bad != 0);
-                if (any) {
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) {
-                        const uint32_t mask = __ballot_sync(kFull, (bad >> j) & 1u);
-                        if (lane == 0) nan_s[slot][wq][j] = mask;
-                    }
-                }
-                if (lane == 0) {
-                    pos_max[slot][wq] = most;
-                    nan_any[slot][wq] = any;
-                }
-                put_token<D>(smem + Sm::kK + st * Sm::kTileBytes, kr, tok, ks);
-                fence_async_smem();
-                mbar_arrive(&bars.k_full[st]);
-                return true;
-            };
-            load_k(0);
-            load_token<D>(vr, vc, vp, row0, row0 < L);
-            bool ok = put_k(0);
-            if (T > 1) load_k(1);
-            for (int t = 0; ok && t < T; ++t) {
-                if (t + 1 < T) {
-                    if (!put_k(t + 1)) break;
-                    if (t + 2 < T) load_k(t + 2);
-                }
-                // the rows that see a NaN group learn of it by nan_s; in a product it
-                // would reach all rows
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    if (vr.par[j] == kNanPar) vr.par[j] = 0;
+            int asked = 0;
+            if (tid == 0)
+                for (; asked < deep && asked < T; ++asked) fetch(asked);
+            uint64_t *full = is_v ? bars.v_full : bars.k_full, *empty = is_v ? bars.v_empty : bars.k_empty;
+            int t = 0;
+            for (; t < T; ++t) {
                 const uint32_t n = n_tiles + t, st = n & 1;
-                if (!wait(&bars.v_empty[st], ((n >> 1) & 1) ^ 1)) break;
-                put_token<D>(smem + Sm::kV + st * Sm::kTileBytes, vr, tok, vs);
+                const unsigned char* raw = raw_at(n);
+                const int64_t left = L - (int64_t)(tile0 + t) * kTok;
+                const int rows = left < kTok ? (int)left : kTok;
+                const uint32_t used = deep == 2 ? n >> 1 : n;   // of this raw tile's barrier
+                if (!wait(&bars.raw_full[is_v][n & (deep - 1)], used & 1)) break;
+                if (!wait(&empty[st], ((n >> 1) & 1) ^ 1)) break;
+                if (is_v) {
+                    // the rows that see a NaN group learn of it by nan_s; in a product it
+                    // would reach all rows
+                    convert<D>(smem + Sm::kV + st * Sm::kTileBytes, raw + Sm::kRawV,
+                               raw + Sm::kRawV + Sm::kCodes, tid, rows, scale, true);
+                } else {
+                    const uint32_t slot = n % kInfo;
+                    const int32_t p = tid < rows ? reinterpret_cast<const int32_t*>(raw + Sm::kRawPos)[tid]
+                                                 : 0x7fffffff;
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        bad |= (reinterpret_cast<const uint32_t*>(raw + Sm::kRawVp)[tid * NG + g] == kNanPar
+                                    ? 1u : 0u) << g;
+                    pos_s[slot][tid] = p;
+                    const int32_t most = __reduce_max_sync(kFull, p);
+                    const bool any = __any_sync(kFull, bad != 0);
+                    if (any) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const uint32_t mask = __ballot_sync(kFull, (bad >> g) & 1u);
+                            if (lane == 0) nan_s[slot][wq][g] = mask;
+                        }
+                    }
+                    if (lane == 0) {
+                        pos_max[slot][wq] = most;
+                        nan_any[slot][wq] = any;
+                    }
+                    convert<D>(smem + Sm::kK + st * Sm::kTileBytes, raw, raw + Sm::kRawKp, tid, rows,
+                               scale, false);
+                }
                 fence_async_smem();
-                mbar_arrive(&bars.v_full[st]);
-                const int64_t row = row0 + (int64_t)(t + 1) * kTok;
-                if (t + 1 < T) load_token<D>(vr, vc, vp, row, row < L);
+                mbar_arrive(&full[st]);
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + is_v) : "memory");   // the raw tile is read
+                if (tid == 0 && asked < T) fetch(asked++);
             }
-            __syncwarp();
+            // after a failure: what was asked for lands before the CTA ends
+            if (t < T && tid == 0)
+                for (; t < asked; ++t)
+                    mbar_wait_bounded(&bars.raw_full[is_v][(n_tiles + t) & (deep - 1)],
+                                      (deep == 2 ? (n_tiles + t) >> 1 : n_tiles + t) & 1,
+                                      c.status, kWaitPollsAfterFail);
         };
         for_units([] {}, work);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
         // ---- products ----
         const uint64_t q0 = sw128(smem_u32(smem + Sm::kQ), 16), k0 = sw128(smem_u32(smem + Sm::kK), 16),
                        v0 = sw128(smem_u32(smem + Sm::kV), Sm::kSlab);
         constexpr uint32_t kTile16 = Sm::kTileBytes / 16;   // descriptors count 16 bytes
         auto work = [&] {
-            if (warp != kMmaWarp || lane != 0) return;
+            if (lane != 0) return;
             constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
             const int X = un.X;
             bool ok = true;
@@ -802,7 +841,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 ok = ok && wait(&bars.k_full[st], (n >> 1) & 1);
                 if (!ok) return;
                 tc_after();
-                const uint64_t qa = q0 + i * kTile16, ka = k0 + st * kTile16;
+                const uint64_t qa = q0 + (two_blocks ? i * kTile16 : 0), ka = k0 + st * kTile16;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     constexpr int slab16 = Sm::kSlab / 16;
@@ -816,8 +855,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             if (X > 1) qk(1);
             for (int x = 0; ok && x < X; ++x) {
                 const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
-                ok = wait(&bars.v_full[st], (n >> 1) & 1) &&
-                     wait(&bars.p_full[i], ((i ? n_x1 : n_x0) + (x >> 1)) & 1);
+                const uint32_t par = ((i ? n_x1 : n_x0) + (x >> 1)) & 1;
+                ok = wait(&bars.v_full[st], (n >> 1) & 1) && wait(&bars.p_full[i], par);
                 if (!ok) break;
                 tc_after();
                 const uint64_t va = v0 + st * kTile16;
@@ -834,8 +873,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         };
         for_units([] {}, work);
         __syncwarp();
-        if (warp == kMmaWarp)
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
