@@ -27,6 +27,8 @@
 // the CTAs.  Tiles behind a block's last position are left out where slots are positions
 // (nothing was evicted).  A unit that is cut leaves partial results (O, m, sum of P), which
 // kv4_join_kernel adds in the order of the CTAs.
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace recsa {
@@ -342,6 +344,21 @@ __device__ __noinline__ uint32_t nan_groups(const int32_t* pos, const uint32_t* 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* status,
+                                       volatile int* failed) {
+    if (mbar_wait_bounded(bar, parity, status, *failed ? kWaitPollsAfterFail : kWaitPolls))
+        return *failed == 0;
+    *failed = 1;
+    return false;
+}
 __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -436,9 +453,9 @@ __device__ __forceinline__ void all_threads() {
 }
 
 // part: [2 * grid] of: O [D / 4][RB] float4, m [RB], l [RB].
-template <int D>
+template <int D, bool TWO>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, Kv4Query qv,
-                                                                     Kv4Scratch sc, int RB) {
+                                                                     Kv4Scratch sc) {
     constexpr int NG = D / 32;
     using Sm = ChunkSmem<D>;
     extern __shared__ unsigned char smem_raw[];
@@ -456,8 +473,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool two_blocks = RB == 256;        // else the streams share their rows
-    const int sh = two_blocks ? 1 : 0;        // tile of product x: x >> sh
+    constexpr int RB = TWO ? 256 : 128;       // TWO: two blocks of rows; else the streams share them
+    constexpr int sh = TWO ? 1 : 0;           // tile of product x: x >> sh
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -491,16 +508,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     const int64_t at0 = blockIdx.x * quota;
     const int64_t at_end = at0 + quota < total ? at0 + quota : total;
 
-    // a wait of this CTA that gave up ends the CTA's work (all waits are bounded)
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_wait_bounded(bar, parity, c.status, failed ? kWaitPollsAfterFail : kWaitPolls))
-            return failed == 0;
-        failed = 1;
-        return false;
+    // All waits are bounded; one that gives up ends the CTA's work.  What is done already
+    // costs one instruction.
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        return mbar_test(&bar, parity) || wait_long(&bar, parity, c.status, &failed);
     };
     // The units of this CTA, by every role in its own branch: stage() before the rows of Q are
     // needed, then work().  Uses of the barriers so far give their parities.
-    uint32_t n_tiles = 0, n_units = 0, n_x0 = 0, n_x1 = 0;
+    uint32_t n_tiles = 0, n_units = 0;
     auto for_units = [&](auto stage, auto work) {
         int64_t at = at0;
         int b = 0;
@@ -528,11 +543,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             stage();
             all_threads();
             work();
-            const int X = un.X;
             at += un.T;
             n_tiles += un.T;
-            n_x0 += (X + 1) / 2;
-            n_x1 += X / 2;
             ++n_units;
             tc_before();
             all_threads();
@@ -547,10 +559,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + stream * 128, to = tmem + lanes + 256 + stream * 128;
         int lim = -1, row = 0;
+        uint32_t s_parity = 0;
         float rsc = 0.0f;
         auto stage = [&] {
             // this thread's row of Q, scaled by a power of two to [2^10, 2^11)
-            row = un.row0 + (two_blocks ? stream * kRowsStream : 0) + r;
+            row = un.row0 + (TWO ? stream * kRowsStream : 0) + r;
             lim = -1;
             unsigned char* qs = smem + Sm::kQ + stream * Sm::kTileBytes;
             const uint4* q = nullptr;    // read twice: the row need not fit the registers
@@ -591,22 +604,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 y.y = as_u(__floats2half2_rn(x[1], x[5]));
                 y.z = as_u(__floats2half2_rn(x[2], x[6]));
                 y.w = as_u(__floats2half2_rn(x[3], x[7]));
-                if (two_blocks || stream == 0) *reinterpret_cast<uint4*>(qs + chunk_of(r, k)) = y;
+                if (TWO || stream == 0) *reinterpret_cast<uint4*>(qs + chunk_of(r, k)) = y;
             }
             fence_async_smem();
         };
         auto work = [&] {
             const int X = un.X, mine = (X - stream + 1) / 2;
             const bool some = __any_sync(kFull, lim >= 0);
-            const uint32_t n_x = stream ? n_x1 : n_x0;
             float m = kKv4MinLog2;
             float2 l2 = make_float2(0.0f, 0.0f);
             uint32_t nanbits = 0;
             bool ok = true;
             for (int j = 0; j < mine; ++j) {
                 const uint32_t slot = (n_tiles + ((2 * j + stream) >> sh)) % kInfo;
-                ok = __all_sync(kFull, wait(&bars.s_full[stream], (n_x + j) & 1));
+                ok = __all_sync(kFull, wait(bars.s_full[stream], s_parity));
                 if (!ok) break;
+                s_parity ^= 1;
                 tc_after();
                 if (some) {
                     const int4 pm = *reinterpret_cast<const int4*>(pos_max[slot]);
@@ -653,14 +666,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             }
             // ---- results ----
             float l = l2.x + l2.y;
-            ok = __all_sync(kFull, ok && wait(&bars.o_full, n_units & 1));
+            ok = __all_sync(kFull, ok && wait(bars.o_full, n_units & 1));
             tc_after();
             const int64_t cta0 = un.start / quota, cta1 = (un.start + un.tiles - 1) / quota;
             const bool whole = cta0 == cta1;
             const int ev = exponent_of(__uint_as_float(c.vmax[un.u]));
             float f0 = 1.0f, f1 = 0.0f;
             float4* other = reinterpret_cast<float4*>(smem + Sm::kK);   // [D / 4][128]: K is done
-            if (!two_blocks) {
+            if (!TWO) {
                 // stream 1 leaves its part of the same rows to stream 0
                 if (stream == 1) {
                     join_m[r] = m;
@@ -688,7 +701,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     nanbits |= join_nan[r];
                 }
             }
-            if ((two_blocks || stream == 0) && some && ok) {
+            if ((TWO || stream == 0) && some && ok) {
                 const bool live = row < un.row_end;
                 const int i = row / c.G, g = row % c.G, rr = row - un.row0;
                 const bool any = l > 0.0f || l != l;
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         // ---- codes to fp16: one warpgroup K and what the softmax needs, one V ----
         const int tid = threadIdx.x & 127, is_v = (warp - kCodeWarp0) >> 2, wq = warp & 3;
         // raw tiles on their way: the second lies where two blocks have their second Q
-        const int deep = two_blocks ? 1 : 2;
+        const int deep = TWO ? 1 : 2;
         auto raw_at = [&](uint32_t n) {
             return smem + (deep == 2 && (n & 1) ? Sm::kQ + Sm::kTileBytes : Sm::kRaw);
         };
@@ -780,8 +793,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 const int64_t left = L - (int64_t)(tile0 + t) * kTok;
                 const int rows = left < kTok ? (int)left : kTok;
                 const uint32_t used = deep == 2 ? n >> 1 : n;   // of this raw tile's barrier
-                if (!wait(&bars.raw_full[is_v][n & (deep - 1)], used & 1)) break;
-                if (!wait(&empty[st], ((n >> 1) & 1) ^ 1)) break;
+                if (!wait(bars.raw_full[is_v][n & (deep - 1)], used & 1)) break;
+                if (!wait(empty[st], ((n >> 1) & 1) ^ 1)) break;
                 if (is_v) {
                     // the rows that see a NaN group learn of it by nan_s; in a product it
                     // would reach all rows
@@ -831,41 +844,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         const uint64_t q0 = sw128(smem_u32(smem + Sm::kQ), 16), k0 = sw128(smem_u32(smem + Sm::kK), 16),
                        v0 = sw128(smem_u32(smem + Sm::kV), Sm::kSlab);
         constexpr uint32_t kTile16 = Sm::kTileBytes / 16;   // descriptors count 16 bytes
+        constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
+        uint32_t kn = 0, vn = 0, p_parity[2] = {0, 0};      // tiles of K and V used so far
         auto work = [&] {
             if (lane != 0) return;
-            constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
             const int X = un.X;
             bool ok = true;
-            auto qk = [&](int x) {
-                const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
-                ok = ok && wait(&bars.k_full[st], (n >> 1) & 1);
-                if (!ok) return;
+            auto qk = [&](auto stream) {
+                constexpr int i = decltype(stream)::value;
+                const uint32_t st = kn & 1;
+                if (!wait(bars.k_full[st], (kn >> 1) & 1)) return false;
                 tc_after();
-                const uint64_t qa = q0 + (two_blocks ? i * kTile16 : 0), ka = k0 + st * kTile16;
+                const uint64_t qa = q0 + (TWO ? i * kTile16 : 0), ka = k0 + st * kTile16;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    constexpr int slab16 = Sm::kSlab / 16;
-                    const int off = (k >> 2) * slab16 + (k & 3) * 2;
+                    const int off = (k >> 2) * (Sm::kSlab / 16) + (k & 3) * 2;
                     mma_ss(tmem + i * 128, qa + off, ka + off, id_qk, k > 0);
                 }
                 commit(&bars.s_full[i]);
-                if (!two_blocks || i) commit(&bars.k_empty[st]);
+                if (!TWO || i) {
+                    commit(&bars.k_empty[st]);
+                    ++kn;
+                }
+                return true;
             };
-            qk(0);
-            if (X > 1) qk(1);
-            for (int x = 0; ok && x < X; ++x) {
-                const uint32_t n = n_tiles + (x >> sh), st = n & 1, i = x & 1;
-                const uint32_t par = ((i ? n_x1 : n_x0) + (x >> 1)) & 1;
-                ok = wait(&bars.v_full[st], (n >> 1) & 1) && wait(&bars.p_full[i], par);
-                if (!ok) break;
+            auto pv = [&](auto stream, bool first, bool more) {
+                constexpr int i = decltype(stream)::value;
+                const uint32_t st = vn & 1;
+                if (!wait(bars.v_full[st], (vn >> 1) & 1) || !wait(bars.p_full[i], p_parity[i])) return false;
+                p_parity[i] ^= 1;
                 tc_after();
                 const uint64_t va = v0 + st * kTile16;
 #pragma unroll
                 for (int k = 0; k < kTok / 16; ++k)
                     mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, va + k * 128, id_pv,
-                           x > 1 || k > 0);
-                if (!two_blocks || i) commit(&bars.v_empty[st]);
-                if (x + 2 < X) qk(x + 2);
+                           k > 0 || !first);
+                if (!TWO || i) {
+                    commit(&bars.v_empty[st]);
+                    ++vn;
+                }
+                return !more || qk(stream);
+            };
+            const std::integral_constant<int, 0> s0;
+            const std::integral_constant<int, 1> s1;
+            ok = qk(s0) && (X < 2 || qk(s1));
+            for (int x = 0; ok && x < X; x += 2) {
+                ok = pv(s0, x == 0, x + 2 < X);
+                if (ok && x + 1 < X) ok = pv(s1, x == 0, x + 3 < X);
             }
             commit(&bars.o_full);
             // after a failure: what was issued is done before TMEM is given back
@@ -948,8 +973,10 @@ int chunk_rows(int rows) { return rows > kRowsStream ? 2 * kRowsStream : kRowsSt
 template <int D>
 cudaError_t chunk_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s) {
     const int rows = qv.w * c.G, RB = chunk_rows(rows);
-    cudaError_t e = kv4_launch(kv4_chunk_kernel<D>, dim3(kChunkGrid), kChunkThreads,
-                               (size_t)ChunkSmem<D>::kBytes, s, c, qv, sc, RB);
+    const size_t smem = ChunkSmem<D>::kBytes;
+    cudaError_t e = RB == 256
+        ? kv4_launch(kv4_chunk_kernel<D, true>, dim3(kChunkGrid), kChunkThreads, smem, s, c, qv, sc)
+        : kv4_launch(kv4_chunk_kernel<D, false>, dim3(kChunkGrid), kChunkThreads, smem, s, c, qv, sc);
     if (e != cudaSuccess) return e;
     return kv4_launch(kv4_join_kernel<D>, dim3((unsigned)((rows + 31) / 32), (unsigned)(c.B * c.Hkv)), 256,
                       0, s, c, qv, sc, RB, kChunkGrid);
@@ -961,14 +988,16 @@ size_t kv4_chunk_part_floats(int D, int rows) {
     return (size_t)2 * kChunkGrid * chunk_rows(rows) * (D + 2);
 }
 
-cudaError_t kv4_prepare_chunk(int D) {
-    return D == 128 ? cudaFuncSetAttribute(kv4_chunk_kernel<128>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           ChunkSmem<128>::kBytes)
-                    : cudaFuncSetAttribute(kv4_chunk_kernel<64>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           ChunkSmem<64>::kBytes);
+template <int D>
+static cudaError_t prepare_impl() {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kv4_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::kBytes);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(kv4_chunk_kernel<D, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   ChunkSmem<D>::kBytes);
 }
+cudaError_t kv4_prepare_chunk(int D) { return D == 128 ? prepare_impl<128>() : prepare_impl<64>(); }
 
 cudaError_t kv4_launch_chunk(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s) {
     NvtxRange nv("recsa kv4 chunk");
