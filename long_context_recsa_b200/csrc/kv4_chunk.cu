@@ -244,6 +244,17 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t (&u)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ void ld16(uint32_t t, uint32_t (&u)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15])
+        : "r"(t)
+        : "memory");
+}
 // When the running maximum moves: the row's sums so far, by f <= 1.
 template <int D>
 __device__ __noinline__ void rescale_o(uint32_t t, float f) {
@@ -283,15 +294,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---- softmax of 32 scores of a row ----
-__device__ __forceinline__ float most_of(const float (&s)[32]) {
-    float x = fmaxf(s[0], s[1]), y = fmaxf(s[2], s[3]);
-#pragma unroll
-    for (int e = 4; e < 32; e += 4) {
-        x = fmaxf(x, fmaxf(s[e], s[e + 1]));
-        y = fmaxf(y, fmaxf(s[e + 2], s[e + 3]));
-    }
-    return fmaxf(x, y);
-}
 // Scores of tokens behind position lim become -infinity, in TMEM.  (Not inlined: the few
 // tiles that need it must not lengthen the loop.  The roles' loops run side by side, and when
 // everything was unrolled the SM's instruction cache missed at 64% of the next level's rate.)
@@ -313,19 +315,47 @@ __device__ __noinline__ void hide_scores(uint32_t t, const int32_t* pos, int lim
     }
     st_done();
 }
-// P = 2^(s * scale + shift) as fp16 to TMEM; its sum in fp32 to l2.
-__device__ __forceinline__ void put_p(uint32_t t, const float (&s)[32], float scale, float shift,
-                                      float2& l2) {
-    uint32_t p[16];
+// p = 2^(s * scale + shift) as fp16 and its sum in fp32; returns the largest.
+__device__ __forceinline__ float form_p(const float (&s)[32], float scale, float shift, uint32_t (&p)[16],
+                                        float2& sum) {
+    float most[2] = {0.0f, 0.0f};
+    float2 l[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         float2 a = fma2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(shift, shift));
         a.x = ex2(a.x);
         a.y = ex2(a.y);
-        l2 = add2(l2, a);
+        const int h = (e >> 1) & 1;
+        l[h] = add2(l[h], a);
+        most[h] = fmaxf(most[h], fmaxf(a.x, a.y));
         p[e >> 1] = as_u(__floats2half2_rn(a.x, a.y));
     }
-    st16(t, p);
+    sum = add2(l[0], l[1]);
+    return fmaxf(most[0], most[1]);
+}
+// Moves the running maximum to that of scores 32 k .. 32 k + 31, where they pass it by more than
+// kGrow; the sixteens of P that the tile already has are scaled by the factor f.
+__device__ __noinline__ float grow(uint32_t ts, int k, float rsc, float m, float& f) {
+    float s[32];
+    ld32(ts + k * 32, s);
+    ld_done(s);
+    float x = s[0];
+#pragma unroll
+    for (int e = 1; e < 32; ++e) x = fmaxf(x, s[e]);
+    x *= rsc;
+    const float mn = x > m + kGrow ? x : m;
+    f = ex2(m - mn);
+    const __half2 h = __float2half2_rn(f);
+    st_done();
+#pragma unroll 1
+    for (int i = 0; i < k; ++i) {
+        uint32_t p[16];
+        ld16(ts + i * 16, p);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = as_u(__hmul2(as_h2(p[e]), h));
+        st16(ts + i * 16, p);
+    }
+    return mn;
 }
 // Groups of dims in which a token that the row sees holds NaN.
 template <int NG>
@@ -628,36 +658,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     if (__any_sync(kFull, most > lim && lim >= 0)) hide_scores(ts, pos_s[slot], lim);
                     if (na.x | na.y | na.z | na.w)
                         nanbits |= nan_groups<NG>(pos_s[slot], nan_any[slot], nan_s[slot], lim);
-                    float mx = -INFINITY;
+                    // P is formed with the old m; should one pass 2^(kUp + kGrow), m moves and
+                    // the 32 scores are read again
 #pragma unroll 1
-                    for (int k = 0; k < kTok; k += 64) {
-                        float a[32], z[32];
-                        ld32(ts + k, a);
-                        ld32(ts + k + 32, z);
-                        ld_done(a);
-                        ld_done(z);
-                        mx = fmaxf(mx, fmaxf(most_of(a), most_of(z)));
-                    }
-                    mx *= rsc;
-                    if (__any_sync(kFull, mx > m + kGrow)) {
-                        const float mn = mx > m + kGrow ? mx : m;
-                        const float f = ex2(m - mn);
-                        m = mn;
-                        l2.x *= f;
-                        l2.y *= f;
-                        // the products before S are done (one thread issued both, and the
-                        // barrier stands for all it had issued)
-                        if (j > 0) rescale_o<D>(to, f);
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < kTok; k += 64) {
-                        float a[32], z[32];
-                        ld32(ts + k, a);
-                        ld32(ts + k + 32, z);
-                        ld_done(a);
-                        ld_done(z);
-                        put_p(ts + k / 2, a, rsc, kUp - m, l2);
-                        put_p(ts + k / 2 + 16, z, rsc, kUp - m, l2);
+                    for (int k = 0; k < kTok / 32;) {
+                        float v[32];
+                        uint32_t p[16];
+                        float2 sum;
+                        ld32(ts + k * 32, v);
+                        ld_done(v);
+                        const float most_p = form_p(v, rsc, kUp - m, p, sum);
+                        if (__any_sync(kFull, most_p > 16384.0f)) {
+                            float f;
+                            m = grow(ts, k, rsc, m, f);
+                            l2.x *= f;
+                            l2.y *= f;
+                            // the products before S are done (one thread issued both, and
+                            // the barrier stands for all it had issued)
+                            if (j > 0) rescale_o<D>(to, f);
+                            continue;
+                        }
+                        l2 = add2(l2, sum);
+                        st16(ts + k * 16, p);
+                        ++k;
                     }
                     st_done();
                 }
