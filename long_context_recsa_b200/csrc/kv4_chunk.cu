@@ -12,12 +12,12 @@
 // even and the odd tiles of the same rows, whose results are joined at the end.
 //
 // Eight warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
-// halves, less 1024 is the code, and one HFMA2 gives lo + s * code, rounded once (2^-12 of
+// halves, less 1024 is the code, and one HFMA2 gives lo + s * code, rounded once (2^-11 of
 // the value).  K, V and q are scaled by powers of two into fp16's range (the largest |K|
 // and |V| of a unit are kept by the writes); a bf16 q is exact there.  P is scaled to at most
-// 2^14: its rounding is 2^-12 relative down to 2^-28 of the largest.  The running maximum m
-// moves only when a score passes it by 6 (in log2), so O is seldom rescaled; m, the sum of
-// P, S and O are fp32.
+// 2^14: its rounding is 2^-11 relative down to 2^-28 of the largest.  The running reference
+// (a score of the row) moves only when a score passes it by 6 (in log2), so O is seldom
+// rescaled; it, the sum of P, S and O are fp32.
 //
 // Bound: 4 d flops a pair of row and token.  At 128 x 128 x 128 a tile and stream, products
 // take 1024 cycles at the tensor cores' rate and the 16384 exponentials 1024 cycles at the
@@ -44,7 +44,8 @@ constexpr int kChunkThreads = 17 * 32;
 constexpr int kInfo = 4;                  // tiles whose positions are held (see the ring's use)
 constexpr uint32_t kNanPar = 0x7fc00000u;   // lo = NaN, s = 0
 constexpr float kUp = 8.0f;               // P is scaled by 2^8, and stays below 2^14
-constexpr float kGrow = 6.0f;
+constexpr float kMostP = 16384.0f;        // P moves the reference where it passes 2^(kUp + 6)
+constexpr float kNoScore = -3e38f;
 
 template <int D>
 struct ChunkSmem {
@@ -315,14 +316,16 @@ __device__ __noinline__ void hide_scores(uint32_t t, const int32_t* pos, int lim
     }
     st_done();
 }
-// p = 2^(s * scale + shift) as fp16 and its sum in fp32; returns the largest.
-__device__ __forceinline__ float form_p(const float (&s)[32], float scale, float shift, uint32_t (&p)[16],
+// p = 2^((s - ref) * scale + kUp) as fp16 and its sum in fp32; returns the largest.  The
+// difference comes first: at ref it is exactly 0, however large the scores are.
+__device__ __forceinline__ float form_p(const float (&s)[32], float scale, float ref, uint32_t (&p)[16],
                                         float2& sum) {
     float most[2] = {0.0f, 0.0f};
     float2 l[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-        float2 a = fma2(make_float2(s[e], s[e + 1]), make_float2(scale, scale), make_float2(shift, shift));
+        float2 a = add2(make_float2(s[e], s[e + 1]), make_float2(-ref, -ref));
+        a = fma2(a, make_float2(scale, scale), make_float2(kUp, kUp));
         a.x = ex2(a.x);
         a.y = ex2(a.y);
         const int h = (e >> 1) & 1;
@@ -333,19 +336,22 @@ __device__ __forceinline__ float form_p(const float (&s)[32], float scale, float
     sum = add2(l[0], l[1]);
     return fmaxf(most[0], most[1]);
 }
-// Moves the running maximum to that of scores 32 k .. 32 k + 31, where they pass it by more than
-// kGrow; the sixteens of P that the tile already has are scaled by the factor f.
-__device__ __noinline__ float grow(uint32_t ts, int k, float rsc, float m, float& f) {
+// Moves the reference of the rows that are `over` to the largest of scores 32 k .. 32 k + 31;
+// the sixteens of P that the tile already has are scaled by the factor, which is returned.
+__device__ __noinline__ float grow(uint32_t ts, int k, float rsc, bool over, float& ref) {
     float s[32];
     ld32(ts + k * 32, s);
     ld_done(s);
-    float x = s[0];
+    float f = 1.0f;
+    if (over) {
+        float x = s[0];
 #pragma unroll
-    for (int e = 1; e < 32; ++e) x = fmaxf(x, s[e]);
-    x *= rsc;
-    const float mn = x > m + kGrow ? x : m;
-    f = ex2(m - mn);
+        for (int e = 1; e < 32; ++e) x = fmaxf(x, s[e]);
+        f = ex2((ref - x) * rsc);
+        ref = x;
+    }
     const __half2 h = __float2half2_rn(f);
+    __syncwarp();
     st_done();
 #pragma unroll 1
     for (int i = 0; i < k; ++i) {
@@ -355,7 +361,7 @@ __device__ __noinline__ float grow(uint32_t ts, int k, float rsc, float m, float
         for (int e = 0; e < 16; ++e) p[e] = as_u(__hmul2(as_h2(p[e]), h));
         st16(ts + i * 16, p);
     }
-    return mn;
+    return f;
 }
 // Groups of dims in which a token that the row sees holds NaN.
 template <int NG>
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         auto work = [&] {
             const int X = un.X, mine = (X - stream + 1) / 2;
             const bool some = __any_sync(kFull, lim >= 0);
-            float m = kKv4MinLog2;
+            float ref = kNoScore;      // of the exponent, in the products' units
             float2 l2 = make_float2(0.0f, 0.0f);
             uint32_t nanbits = 0;
             bool ok = true;
@@ -658,8 +664,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     if (__any_sync(kFull, most > lim && lim >= 0)) hide_scores(ts, pos_s[slot], lim);
                     if (na.x | na.y | na.z | na.w)
                         nanbits |= nan_groups<NG>(pos_s[slot], nan_any[slot], nan_s[slot], lim);
-                    // P is formed with the old m; should one pass 2^(kUp + kGrow), m moves and
-                    // the 32 scores are read again
+                    // P is formed with the old reference; should one pass kMostP, that
+                    // moves and the 32 scores are read once more (then none can pass it)
+                    bool moved = false;
 #pragma unroll 1
                     for (int k = 0; k < kTok / 32;) {
                         float v[32];
@@ -667,17 +674,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                         float2 sum;
                         ld32(ts + k * 32, v);
                         ld_done(v);
-                        const float most_p = form_p(v, rsc, kUp - m, p, sum);
-                        if (__any_sync(kFull, most_p > 16384.0f)) {
-                            float f;
-                            m = grow(ts, k, rsc, m, f);
+                        const bool over = form_p(v, rsc, ref, p, sum) > kMostP;
+                        if (__any_sync(kFull, over) && !moved) {
+                            const float f = grow(ts, k, rsc, over, ref);
                             l2.x *= f;
                             l2.y *= f;
                             // the products before S are done (one thread issued both, and
                             // the barrier stands for all it had issued)
                             if (j > 0) rescale_o<D>(to, f);
+                            moved = true;
                             continue;
                         }
+                        moved = false;
                         l2 = add2(l2, sum);
                         st16(ts + k * 16, p);
                         ++k;
@@ -689,6 +697,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             }
             // ---- results ----
             float l = l2.x + l2.y;
+            float m = l == 0.0f ? kKv4MinLog2 : ref * rsc;
             ok = __all_sync(kFull, ok && wait(bars.o_full, n_units & 1));
             tc_after();
             const int64_t cta0 = un.start / quota, cta1 = (un.start + un.tiles - 1) / quota;
