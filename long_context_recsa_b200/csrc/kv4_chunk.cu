@@ -190,6 +190,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
+// One thread of a whole warp, the same each time (a commit stands for what its thread issued).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 // Arrives on `bar` when all products that this thread has issued are done.
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -879,25 +885,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
         constexpr uint32_t id_qk = f16_idesc(kTok, false), id_pv = f16_idesc(D, true);
         uint32_t kn = 0, vn = 0, p_parity[2] = {0, 0};      // tiles of K and V used so far
         auto work = [&] {
-            if (lane != 0) return;
-            const int X = un.X;
+            // the whole warp goes through the loop, one elected thread issues
+            const int X = __shfl_sync(kFull, un.X, 0);
             bool ok = true;
             auto qk = [&](auto stream) {
                 constexpr int i = decltype(stream)::value;
                 const uint32_t st = kn & 1;
                 if (!wait(bars.k_full[st], (kn >> 1) & 1)) return false;
                 tc_after();
-                const uint64_t qa = q0 + (TWO ? i * kTile16 : 0), ka = k0 + st * kTile16;
+                if (elect_one()) {
+                    const uint64_t qa = q0 + (TWO ? i * kTile16 : 0), ka = k0 + st * kTile16;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int off = (k >> 2) * (Sm::kSlab / 16) + (k & 3) * 2;
-                    mma_ss(tmem + i * 128, qa + off, ka + off, id_qk, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int off = (k >> 2) * (Sm::kSlab / 16) + (k & 3) * 2;
+                        mma_ss(tmem + i * 128, qa + off, ka + off, id_qk, k > 0);
+                    }
+                    commit(&bars.s_full[i]);
+                    if (!TWO || i) commit(&bars.k_empty[st]);
                 }
-                commit(&bars.s_full[i]);
-                if (!TWO || i) {
-                    commit(&bars.k_empty[st]);
-                    ++kn;
-                }
+                __syncwarp();
+                if (!TWO || i) ++kn;
                 return true;
             };
             auto pv = [&](auto stream, bool first, bool more) {
@@ -906,15 +913,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 if (!wait(bars.v_full[st], (vn >> 1) & 1) || !wait(bars.p_full[i], p_parity[i])) return false;
                 p_parity[i] ^= 1;
                 tc_after();
-                const uint64_t va = v0 + st * kTile16;
+                if (elect_one()) {
+                    const uint64_t va = v0 + st * kTile16;
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, va + k * 128, id_pv,
-                           k > 0 || !first);
-                if (!TWO || i) {
-                    commit(&bars.v_empty[st]);
-                    ++vn;
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, va + k * 128, id_pv,
+                               k > 0 || !first);
+                    if (!TWO || i) commit(&bars.v_empty[st]);
                 }
+                __syncwarp();
+                if (!TWO || i) ++vn;
                 return !more || qk(stream);
             };
             const std::integral_constant<int, 0> s0;
@@ -924,7 +932,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 ok = pv(s0, x == 0, x + 2 < X);
                 if (ok && x + 1 < X) ok = pv(s1, x == 0, x + 3 < X);
             }
-            commit(&bars.o_full);
+            if (elect_one()) commit(&bars.o_full);
+            __syncwarp();
             // after a failure: what was issued is done before TMEM is given back
             if (!ok) mbar_wait_bounded(&bars.o_full, n_units & 1, c.status, kWaitPollsAfterFail);
         };
