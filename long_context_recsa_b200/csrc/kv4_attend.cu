@@ -99,24 +99,51 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero accumulators (which then need no registers).
+__device__ __forceinline__ void mma16816_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
+    const float z = 0.0f;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+}
+__device__ __forceinline__ void mma16816_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                uint32_t a3, uint32_t b0, uint32_t b1) {
+    const float z = 0.0f;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
 }
-// code - 8 of the low nibble of both halves as normal fp16 numbers: 1024 + code, less 1032.
-__device__ __forceinline__ uint32_t centre_lo(uint32_t x) {
-    x = (x & 0x000f000fu) | 0x64006400u;
-    const uint32_t m = 0xe408e408u;
-    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&m));
-    return *reinterpret_cast<const uint32_t*>(&a);
-}
-// The same of the nibble above it: 64 + code, less 72.
-__device__ __forceinline__ uint32_t centre_hi(uint32_t x) {
-    x = (x & 0x00f000f0u) | 0x54005400u;
-    const uint32_t m = 0xd480d480u;
-    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&m));
-    return *reinterpret_cast<const uint32_t*>(&a);
-}
+// code - 8 of a nibble of both halves as normal fp16 numbers: the low nibble joined to 1024,
+// less 1032; the nibble above it joined to 64, less 72.  The exponents come from registers
+// (an instruction takes one immediate, the mask).
+struct Centre {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Centre() {
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(lo));
+        asm volatile("mov.b32 %0, 0x54005400;" : "=r"(hi));
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t x) const {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;\n\tadd.rn.f16x2 %0, %0, %3;"
+            : "=r"(y) : "r"(x), "r"(lo), "r"(0xe408e408u));
+        return y;
+    }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;\n\tadd.rn.f16x2 %0, %0, %3;"
+            : "=r"(y) : "r"(x), "r"(hi), "r"(0xd480d480u));
+        return y;
+    }
+};
 // (without .ftz every call is wrapped in the scaling of subnormal results)
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -143,7 +170,8 @@ struct Rows {
     static constexpr int NG = D / kKv4Group;
     static constexpr int RB = NCS * 8 / T;
     uint4 frag[NCS][NG][32];         // B operands of the two MMAs of a group, by lane
-    float sum[RB][NG];               // sums of q over a group, in the MMAs' scale
+    float sum[RB][NG];               // fp32 tensors: sums of q over a group
+    uint2 off[32];                   // bf16: the same sums as the offsets' B operand, by lane
     float scale[RB];                 // accumulator -> score in log2 units
     int lim[RB];                     // last position the row sees, -1: no row
 };
@@ -154,7 +182,7 @@ template <int D, int T, int NCS>
 __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query& qv, int b, int h,
                            int row0, int row_end, int n_b, int64_t seen, int warp, int nwarps,
                            int lane) {
-    constexpr int RB = NCS * 8 / T, E = D / 32;
+    constexpr int RB = NCS * 8 / T, E = D / 32, NG = D / kKv4Group;
     using TI = typename std::conditional<T == 1, __nv_bfloat16, float>::type;
     for (int r = warp; r < RB; r += nwarps) {
         const int row = row0 + r, i = row / c.G, g = row % c.G;
@@ -184,7 +212,23 @@ __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query
         // the sum over the group's 32 / E lanes
 #pragma unroll
         for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (lane % (32 / E) == 0) rs.sum[r][lane / (32 / E)] = T == 1 ? sum * 0x1p-24f : sum;
+        if (lane % (32 / E) == 0) {
+            const int j = lane / (32 / E);
+            if constexpr (T == 1) {
+                // three bf16 parts (24 bits) meet one bf16 offset
+                const float x0 = sum * 0x1p-24f;
+                const __nv_bfloat16 h = __float2bfloat16_rn(x0);
+                const float x1 = x0 - __bfloat162float(h);
+                const __nv_bfloat16 m = __float2bfloat16_rn(x1);
+                const __nv_bfloat162 a = __halves2bfloat162(h, m);
+                const __nv_bfloat162 z = __floats2bfloat162_rn(x1 - __bfloat162float(m), 0.0f);
+                rs.off[r * 4 + j] = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                               *reinterpret_cast<const uint32_t*>(&z));
+            } else {
+                rs.sum[r][j] = sum;
+            }
+        }
+        if (T == 1 && NG == 2 && lane >= 2 && lane < 4) rs.off[r * 4 + lane] = make_uint2(0, 0);
         if (lane == 0) {
             rs.scale[r] = fminf(c.scale * 1.4426950408889634f * pow2i(ex - 10) * (T == 1 ? 0x1p24f : 1.0f), 3e38f);
             rs.lim[r] = live ? (int)(seen - n_b + i) : -1;
@@ -221,21 +265,39 @@ __device__ __forceinline__ void load_pars(uint32_t (&p)[NG], const unsigned char
     }
 }
 
-// Scores of 16 tokens (rows r0 .. r0 + 15 of a tile at `kc`) against every column set, in
+// Scores of 16 tokens (rows r0 .. r0 + 15 of a tile at `st`) against every column set, in
 // the rows' scale: sc[c][2 * e + k] for the lane's row e and token g (k = 0) or g + 8.
+// bf16 (one column set): lo . sum(q) is a product of its own, the K dimension the groups, four
+// places each: the offset stands in all four (bf16, exact), the sum's parts in three.
 template <int D, int T, int NCS>
-__device__ __forceinline__ void scores16(float (&sc)[NCS][2 * (2 / T)], uint32_t kc,
-                                         const uint32_t (&p0)[D / 32], const uint32_t (&p1)[D / 32],
+__device__ __forceinline__ void scores16(float (&sc)[NCS][2 * (2 / T)], const unsigned char* st,
                                          const Rows<D, T, NCS>& rs,
                                          const uint4 (&qreg)[NCS == 1 ? D / 32 : 1],
                                          const float (&qsum)[NCS == 1 ? 2 / T : 1][D / 32],
-                                         int r0, int lane) {
+                                         uint2 qoff, const Centre& ctr, int r0, int lane) {
     constexpr int NG = D / kKv4Group, RL = 2 / T;
-    const int t = lane & 3;
+    static_assert(T == 2 || NCS == 1, "bf16 rows past one column set go to the chunk kernel");
+    const int t = lane & 3, g = lane >> 2;
+    const uint32_t kc = smem_u32(st + Stage<D>::kK);
+    uint32_t p0[NG], p1[NG];
+    load_pars<NG>(p0, st + Stage<D>::kKp, r0 + g);
+    load_pars<NG>(p1, st + Stage<D>::kKp, r0 + g + 8);
+    if constexpr (T == 1) {
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(st + Stage<D>::kKp) + t % NG;
+        const uint32_t x0 = __byte_perm(par[(r0 + g) * NG], 0, 0x3232);
+        const uint32_t x1 = __byte_perm(par[(r0 + g + 8) * NG], 0, 0x3232);
+        float acc[4];
+        mma16816_bf16_0(acc, x0, x1, x0, x1, qoff.x, qoff.y);
+        sc[0][0] = acc[0];
+        sc[0][2] = acc[1];
+        sc[0][1] = acc[2];
+        sc[0][3] = acc[3];
+    } else {
 #pragma unroll
-    for (int c = 0; c < NCS; ++c)
+        for (int c = 0; c < NCS; ++c)
 #pragma unroll
-        for (int e = 0; e < 2 * RL; ++e) sc[c][e] = 0.0f;
+            for (int e = 0; e < 2 * RL; ++e) sc[c][e] = 0.0f;
+    }
 #pragma unroll
     for (int j2 = 0; j2 < NG; j2 += 2) {
         uint32_t w[4];   // tokens 0-7 and 8-15 of group j2, then of j2 + 1
@@ -243,38 +305,31 @@ __device__ __forceinline__ void scores16(float (&sc)[NCS][2 * (2 / T)], uint32_t
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             const int j = j2 + jj;
-            const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
-            uint32_t a[8];
-            float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
-            float o0 = kv4_off(p0[j]), o1 = kv4_off(p1[j]);
+            const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1], va = wa >> 8, vb = wb >> 8;
+            const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
             if constexpr (T == 1) {
-                a[0] = wa & 0x000f000fu; a[1] = wb & 0x000f000fu;
-                a[2] = wa & 0x00f000f0u; a[3] = wb & 0x00f000f0u;
-                a[4] = (wa >> 8) & 0x000f000fu; a[5] = (wb >> 8) & 0x000f000fu;
-                a[6] = (wa >> 8) & 0x00f000f0u; a[7] = (wb >> 8) & 0x00f000f0u;
+                float acc[4];
+                mma16816_0(acc, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
+                           qreg[j].x, qreg[j].y);
+                mma16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u,
+                         qreg[j].z, qreg[j].w);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[0][2 * e] = fmaf(s0, acc[e], sc[0][2 * e]);
+                    sc[0][2 * e + 1] = fmaf(s1, acc[2 + e], sc[0][2 * e + 1]);
+                }
             } else {
-                a[0] = centre_lo(wa); a[1] = centre_lo(wb);
-                a[2] = centre_hi(wa); a[3] = centre_hi(wb);
-                a[4] = centre_lo(wa >> 8); a[5] = centre_lo(wb >> 8);
-                a[6] = centre_hi(wa >> 8); a[7] = centre_hi(wb >> 8);
-                o0 = fmaf(8.0f, s0, o0);
-                o1 = fmaf(8.0f, s1, o1);
-            }
+                // fp32: centred codes, so that the two terms of a score stay small
+                const uint32_t a[8] = {ctr.low(wa), ctr.low(wb), ctr.high(wa), ctr.high(wb),
+                                       ctr.low(va), ctr.low(vb), ctr.high(va), ctr.high(vb)};
+                const float o0 = fmaf(8.0f, s0, kv4_off(p0[j])), o1 = fmaf(8.0f, s1, kv4_off(p1[j]));
 #pragma unroll
-            for (int c = 0; c < NCS; ++c) {
-                uint4 q;
-                if constexpr (NCS == 1) q = qreg[j]; else q = rs.frag[c][j][lane];
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(acc, a[0], a[1], a[2], a[3], q.x, q.y);
-                mma16816(acc, a[4], a[5], a[6], a[7], q.z, q.w);
-                if constexpr (T == 1) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float qs = NCS == 1 ? qsum[e][j] : rs.sum[c * 8 + 2 * t + e][j];
-                        sc[c][2 * e] = fmaf(s0, acc[e], fmaf(o0, qs, sc[c][2 * e]));
-                        sc[c][2 * e + 1] = fmaf(s1, acc[2 + e], fmaf(o1, qs, sc[c][2 * e + 1]));
-                    }
-                } else {
+                for (int c = 0; c < NCS; ++c) {
+                    uint4 q;
+                    if constexpr (NCS == 1) q = qreg[j]; else q = rs.frag[c][j][lane];
+                    float acc[4];
+                    mma16816_0(acc, a[0], a[1], a[2], a[3], q.x, q.y);
+                    mma16816(acc, a[4], a[5], a[6], a[7], q.z, q.w);
                     const float qs = NCS == 1 ? qsum[0][j] : rs.sum[c * 4 + t][j];
                     sc[c][0] = fmaf(s0, acc[0] + acc[1], fmaf(o0, qs, sc[c][0]));
                     sc[c][1] = fmaf(s1, acc[2] + acc[3], fmaf(o1, qs, sc[c][1]));
@@ -377,6 +432,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
     uint32_t phase = 0;                                // bit s: parity of stage s
     bool alive = true;                                 // no wait of this warp gave up
     unsigned char* my_ring = ring + warp * kStagesKv4 * St::kBytes;
+    const Centre ctr;
 
     int b = 0;
     while (at < at_end) {
@@ -444,9 +500,10 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
             for (int j = 0; j < NG; ++j) {
                 qreg[j] = rs.frag[0][j][lane];
 #pragma unroll
-                for (int e = 0; e < RL; ++e) qsum[e][j] = rs.sum[t * RL + e][j];
+                for (int e = 0; e < RL; ++e) qsum[e][j] = T == 2 ? rs.sum[t * RL + e][j] : 0.0f;
             }
         }
+        const uint2 qoff = rs.off[lane];
 
         for (int it = 0; it < mine; ++it) {
             const int s = it % kStagesKv4;
@@ -466,10 +523,8 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                 const int64_t tok = (int64_t)tile * kTile + r0 + g;
                 if (tail && tok - g >= L) break;       // nothing in this half (uniform)
                 uint32_t p0[NG], p1[NG];
-                load_pars<NG>(p0, st + St::kKp, r0 + g);
-                load_pars<NG>(p1, st + St::kKp, r0 + g + 8);
                 float sc[NCS][2 * RL];
-                scores16<D, T, NCS>(sc, sa + St::kK, p0, p1, rs, qreg, qsum, r0, lane);
+                scores16<D, T, NCS>(sc, st, rs, qreg, qsum, qoff, ctr, r0, lane);
                 load_pars<NG>(p0, st + St::kVp, r0 + g);
                 load_pars<NG>(p1, st + St::kVp, r0 + g + 8);
                 int pos0 = -1, pos1 = -1;
@@ -541,6 +596,11 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         sc[cs][2 * e + 1] = ex2(sc[cs][2 * e + 1] - m[cs][e]);
                         l[cs][e] += sc[cs][2 * e] + sc[cs][2 * e + 1];
                     }
+                float pv[NCS][2 * RL];         // in the scale of P'
+#pragma unroll
+                for (int cs = 0; cs < NCS; ++cs)
+#pragma unroll
+                    for (int e = 0; e < 2 * RL; ++e) pv[cs][e] = sc[cs][e] * vf;
                 uint32_t nan0 = 0, nan1 = 0;
 #pragma unroll
                 for (int j2 = 0; j2 < NG; j2 += 2) {
@@ -551,14 +611,14 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         const int j = j2 + jj;
                         const uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
                         // dims 4g + k of the group, tokens 2t, 2t + 1 (wa) and + 8 (wb)
-                        const uint32_t a0 = centre_lo(wa);
-                        const uint32_t a1 = centre_hi(wa);
-                        const uint32_t a2 = centre_lo(wb);
-                        const uint32_t a3 = centre_hi(wb);
-                        const uint32_t a4 = centre_lo(wa >> 8);
-                        const uint32_t a5 = centre_hi(wa >> 8);
-                        const uint32_t a6 = centre_lo(wb >> 8);
-                        const uint32_t a7 = centre_hi(wb >> 8);
+                        const uint32_t a0 = ctr.low(wa);
+                        const uint32_t a1 = ctr.high(wa);
+                        const uint32_t a2 = ctr.low(wb);
+                        const uint32_t a3 = ctr.high(wb);
+                        const uint32_t a4 = ctr.low(wa >> 8);
+                        const uint32_t a5 = ctr.high(wa >> 8);
+                        const uint32_t a6 = ctr.low(wb >> 8);
+                        const uint32_t a7 = ctr.high(wb >> 8);
                         const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
                         float c0 = fmaf(8.0f, s0, kv4_off(p0[j]));
                         float c1 = fmaf(8.0f, s1, kv4_off(p1[j]));
@@ -567,15 +627,14 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                             if (c0 != c0) { c0 = 0.0f; nan0 |= 1u << j; }
                             if (c1 != c1) { c1 = 0.0f; nan1 |= 1u << j; }
                         }
-                        const float f0 = s0 * vf, f1 = s1 * vf;
 #pragma unroll
                         for (int cs = 0; cs < NCS; ++cs) {
                             uint32_t b0, b1;
                             if constexpr (T == 1) {
-                                b0 = movm(pack_h2(sc[cs][0] * f0, sc[cs][2] * f0));
-                                b1 = movm(pack_h2(sc[cs][1] * f1, sc[cs][3] * f1));
+                                b0 = movm(pack_h2(pv[cs][0] * s0, pv[cs][2] * s0));
+                                b1 = movm(pack_h2(pv[cs][1] * s1, pv[cs][3] * s1));
                             } else {
-                                const float x0 = sc[cs][0] * f0, x1 = sc[cs][1] * f1;
+                                const float x0 = pv[cs][0] * s0, x1 = pv[cs][1] * s1;
                                 const float h0 = __half2float(__float2half_rn(x0));
                                 const float h1 = __half2float(__float2half_rn(x1));
                                 b0 = movm(pack_h2(h0, (x0 - h0) * kLowUp));
@@ -818,6 +877,7 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     uint32_t phase = 0;
     bool alive = true;
     unsigned char* my_ring = ring + warp * kStagesKv4 * St::kBytes;
+    const Centre ctr;
     int b = 0;
     while (at < at_end) {
         while (pl.pre[b + 1] <= at) ++b;
@@ -875,9 +935,6 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                 const int r0 = half * 16;
                 const int64_t tok = (int64_t)tile * kTile + r0 + g;
                 if (tok - g >= L) break;
-                uint32_t p0[NG], p1[NG];
-                load_pars<NG>(p0, st + St::kKp, r0 + g);
-                load_pars<NG>(p1, st + St::kKp, r0 + g + 8);
                 int pos0 = -1, pos1 = -1;
                 if (CHUNK) {
                     pos0 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g) * 4);
@@ -893,10 +950,10 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                     for (int j = 0; j < NG; ++j) {
                         qreg[j] = rs[k].frag[0][j][lane];
 #pragma unroll
-                        for (int e = 0; e < RL; ++e) qsum[e][j] = rs[k].sum[t * RL + e][j];
+                        for (int e = 0; e < RL; ++e) qsum[e][j] = T == 2 ? rs[k].sum[t * RL + e][j] : 0.0f;
                     }
                     float sc[1][2 * RL];
-                    scores16<D, T, 1>(sc, sa + St::kK, p0, p1, rs[k], qreg, qsum, r0, lane);
+                    scores16<D, T, 1>(sc, st, rs[k], qreg, qsum, rs[k].off[lane], ctr, r0, lane);
 #pragma unroll
                     for (int e = 0; e < RL; ++e) {
                         const float f = rs[k].scale[t * RL + e], ls = lse[k * RB + t * RL + e];
@@ -964,8 +1021,10 @@ cudaError_t prepare_impl() {
     if constexpr (T == 2)
         if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, false>, attend_smem<D, T, 2>());
     if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 1, true>, attend_smem<D, T, 1>());
-    if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, true>, attend_smem<D, T, 2>());
-    if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 4, true>, attend_smem<D, T, 4>());
+    if constexpr (T == 2) {
+        if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, true>, attend_smem<D, T, 2>());
+        if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 4, true>, attend_smem<D, T, 4>());
+    }
     if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false>, weights_smem<D, T>(kWeightBlocks));
     if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true>, weights_smem<D, T>(kWeightBlocks));
     return e;
@@ -989,11 +1048,14 @@ cudaError_t attend_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& 
     if (sets == 1)
         return kv4_launch(kv4_attend_kernel<D, T, 1, true>, grid, kAttendThreads,
                           attend_smem<D, T, 1>(), s, c, qv, sc, maps);
-    if (sets == 2)
-        return kv4_launch(kv4_attend_kernel<D, T, 2, true>, grid, kAttendThreads,
-                          attend_smem<D, T, 2>(), s, c, qv, sc, maps);
-    return kv4_launch(kv4_attend_kernel<D, T, 4, true>, grid, kAttendThreads,
-                      attend_smem<D, T, 4>(), s, c, qv, sc, maps);
+    if constexpr (T == 2) {
+        if (sets == 2)
+            return kv4_launch(kv4_attend_kernel<D, T, 2, true>, grid, kAttendThreads,
+                              attend_smem<D, T, 2>(), s, c, qv, sc, maps);
+        return kv4_launch(kv4_attend_kernel<D, T, 4, true>, grid, kAttendThreads,
+                          attend_smem<D, T, 4>(), s, c, qv, sc, maps);
+    }
+    return cudaErrorInvalidValue;   // more bf16 rows are the chunk kernel's
 }
 
 template <int D, int T>
