@@ -57,9 +57,9 @@ struct Stage {
     static constexpr int kCodes = kTile * D / 2;
     static constexpr int kPars = kTile * D / 8;
     static constexpr int kK = 0, kV = kCodes, kKp = 2 * kCodes, kVp = 2 * kCodes + kPars;
-    static constexpr int kPos = 2 * kCodes + 2 * kPars;
+    static constexpr int kPos = 2 * kCodes + 2 * kPars, kW = kPos + kTile * 4;
     // a multiple of the swizzle pattern (512 bytes for 64-byte rows, 256 for 32-byte)
-    static constexpr int kBytes = ((kPos + kTile * 4) + 511) / 512 * 512;
+    static constexpr int kBytes = ((kW + kTile * 4) + 511) / 512 * 512;
 };
 
 // Byte offset of 16-byte chunk `ch` (one group) of row r in a swizzled tile.
@@ -176,27 +176,41 @@ struct Rows {
     int lim[RB];                     // last position the row sees, -1: no row
 };
 
-// Stages rows row0 .. row0 + RB - 1 of (b, h) (row = chunk row * G + head of the group).
-// One warp per row in turn; `n_b` rows of the sequence are in use, positions end at `seen`.
+// Stages rows row0 .. row0 + blocks * RB - 1 of (b, h) (row = chunk row * G + head of the group)
+// into as many blocks.  A warp takes a row in turn, four loaded before the first is used (one
+// at a time, staging 128 rows took longer than the weights' products over them); `n_b` rows
+// of the sequence are in use, positions end at `seen`.
 template <int D, int T, int NCS>
-__device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query& qv, int b, int h,
-                           int row0, int row_end, int n_b, int64_t seen, int warp, int nwarps,
-                           int lane) {
+__device__ void stage_rows(Rows<D, T, NCS>* blocks_of, int blocks, const Kv4View& c, const Kv4Query& qv,
+                           int b, int h, int row0, int row_end, int n_b, int64_t seen, int warp,
+                           int nwarps, int lane) {
     constexpr int RB = NCS * 8 / T, E = D / 32, NG = D / kKv4Group;
     using TI = typename std::conditional<T == 1, __nv_bfloat16, float>::type;
-    for (int r = warp; r < RB; r += nwarps) {
-        const int row = row0 + r, i = row / c.G, g = row % c.G;
-        const bool live = row < row_end && i < n_b;
-        float x[E];                  // dims lane * E ..: a group is 32 / E lanes
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int r0 = warp; r0 < blocks * RB; r0 += kBatch * nwarps) {
+    float q[kBatch][E];              // dims lane * E ..: a group is 32 / E lanes
+    int at[kBatch];                  // last position the row sees, -1: no row
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int row = row0 + r0 + k * nwarps, i = row / c.G, g = row % c.G;
+        const bool live = r0 + k * nwarps < blocks * RB && row < row_end && i < n_b;
+        at[k] = live ? (int)(seen - n_b + i) : -1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[k][e] = 0.0f;
         if (live) {
-            const TI* q = reinterpret_cast<const TI*>(qv.q) +
+            const TI* p = reinterpret_cast<const TI*>(qv.q) +
                           (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = (float)q[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.0f;
+            for (int e = 0; e < E; ++e) q[k][e] = (float)p[e];
         }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        if (r0 + k * nwarps >= blocks * RB) break;
+        Rows<D, T, NCS>& rs = blocks_of[(r0 + k * nwarps) / RB];
+        const int r = (r0 + k * nwarps) % RB;
+        float(&x)[E] = q[k];
         float mx = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
@@ -231,16 +245,16 @@ __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query
         if (T == 1 && NG == 2 && lane >= 2 && lane < 4) rs.off[r * 4 + lane] = make_uint2(0, 0);
         if (lane == 0) {
             rs.scale[r] = fminf(c.scale * 1.4426950408889634f * pow2i(ex - 10) * (T == 1 ? 0x1p24f : 1.0f), 3e38f);
-            rs.lim[r] = live ? (int)(seen - n_b + i) : -1;
+            rs.lim[r] = at[k];
         }
         // dim 8t + k of a group (k < 8) sits in 16-bit unit (k >> 1 with the pairs
         // (0,4), (1,5), (2,6), (3,7)) of lane (column, t); odd pairs meet codes * 16
         __half* f = reinterpret_cast<__half*>(&rs.frag[r / (8 / T)][0][0]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int dim = lane * E + e, grp = dim / 32, t = (dim / 8) & 3, k = dim & 7;
-            const float y = T == 1 && (k & 1) ? x[e] * 0.0625f : x[e];
-            const int reg = k & 3, half = k >> 2;
+            const int dim = lane * E + e, grp = dim / 32, t = (dim / 8) & 3, d8 = dim & 7;
+            const float y = T == 1 && (d8 & 1) ? x[e] * 0.0625f : x[e];
+            const int reg = d8 & 3, half = d8 >> 2;
             if constexpr (T == 1) {
                 const int l = (r & 7) * 4 + t;
                 f[((grp * 32 + l) * 4 + reg) * 2 + half] = __float2half_rn(y);
@@ -251,6 +265,7 @@ __device__ void stage_rows(Rows<D, T, NCS>& rs, const Kv4View& c, const Kv4Query
                 f[((grp * 32 + l + 4) * 4 + reg) * 2 + half] = __float2half_rn(y - __half2float(hi));
             }
         }
+    }
     }
 }
 
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         const int mine = L > 0 ? (tile1 - tile0 - warp + kAttendWarps - 1) / kAttendWarps : 0;
         if (lane == 0 && alive)
             for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + warp + s * kAttendWarps, s);
-        stage_rows<D, T, NCS>(rs, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp, kAttendWarps, lane);
+        stage_rows<D, T, NCS>(&rs, 1, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp, kAttendWarps, lane);
         __syncthreads();
 
         // V's steps enter P' scaled so that the unit's largest is at most 2^8
@@ -898,8 +913,9 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
             unsigned char* st = my_ring + s * St::kBytes;
             uint64_t* bar = &bars[warp][s];
             const int64_t r = (int64_t)tile * kTile;
-            mbar_expect_tx(bar, St::kCodes + St::kPars + (CHUNK ? kTile * 4 : 0));
+            mbar_expect_tx(bar, St::kCodes + St::kPars + (CHUNK ? 2 : 1) * kTile * 4);
             tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
+            bulk_g2s(st + St::kW, c.w + u * c.R + r, kTile * 4, bar);
             bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
             if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
         };
@@ -907,16 +923,11 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         if (lane == 0 && alive)
             for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + warp + s * kAttendWarps, s);
         if (row0 < row_end) {
-            for (int k = 0; k < n_blocks; ++k) {
-                stage_rows<D, T, 1>(rs[k], c, qv, b, h, row0 + k * RB, row_end, n_b, c.seen[b], warp,
-                                    kAttendWarps, lane);
-                const int i = threadIdx.x;
-                if (i < RB) {
-                    const int row = row0 + k * RB + i;
-                    lse[k * RB + i] = row < row_end
-                        ? sc_.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] : INFINITY;
-                }
-            }
+            stage_rows<D, T, 1>(rs, n_blocks, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp,
+                                kAttendWarps, lane);
+            for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads)
+                lse[i] = row0 + i < row_end
+                    ? sc_.lse[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G] : INFINITY;
         }
         __syncthreads();
         for (int it = 0; it < mine; ++it) {
@@ -969,9 +980,11 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                 sum0 += __shfl_xor_sync(kFull, sum0, 2);
                 sum1 += __shfl_xor_sync(kFull, sum1, 2);
                 if (t == 0) {
+                    // this warp's alone: what the tile brought, and more
+                    const float* old = reinterpret_cast<const float*>(st + St::kW) + r0 + g;
                     float* w = c.w + u * c.R + tok;
-                    if (tok < L) w[0] += sum0;
-                    if (tok + 8 < L) w[8] += sum1;
+                    if (tok < L) w[0] = old[0] + sum0;
+                    if (tok + 8 < L) w[8] = old[8] + sum1;
                 }
             }
             __syncwarp();
@@ -1001,7 +1014,12 @@ constexpr size_t weights_smem(int blocks) {
     return 1024 + (size_t)kAttendWarps * kStagesKv4 * Stage<D>::kBytes +
            (size_t)blocks * (sizeof(Rows<D, T, 1>) + sizeof(float) * 8 / T);
 }
-constexpr int kWeightBlocks = 16;    // column sets a weights launch holds
+// Column sets a weights launch holds: 64 KB of rows, so that two CTAs share an SM beside
+// their rings (four with half of it).
+template <int D, int T>
+constexpr int weight_blocks() {
+    return 65536 / (int)(sizeof(Rows<D, T, 1>) + sizeof(float) * 8 / T);
+}
 
 // Column sets of a block: the fewest that hold the rows, up to four (the accumulators of
 // four fill the register file).
@@ -1025,8 +1043,8 @@ cudaError_t prepare_impl() {
         if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, true>, attend_smem<D, T, 2>());
         if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 4, true>, attend_smem<D, T, 4>());
     }
-    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false>, weights_smem<D, T>(kWeightBlocks));
-    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true>, weights_smem<D, T>(kWeightBlocks));
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false>, weights_smem<D, T>(weight_blocks<D, T>()));
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true>, weights_smem<D, T>(weight_blocks<D, T>()));
     return e;
 }
 
@@ -1062,14 +1080,17 @@ template <int D, int T>
 cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
                          const Kv4Maps& maps, int chunk, cudaStream_t s) {
     const int rows = (qv.acc_rows < qv.w ? qv.acc_rows : qv.w) * c.G, per = 8 / T;
-    for (int r = 0; r < rows; r += kWeightBlocks * per) {
+    constexpr int most = weight_blocks<D, T>();
+    for (int r = 0; r < rows; r += most * per) {
         int blocks = (rows - r + per - 1) / per;
-        if (blocks > kWeightBlocks) blocks = kWeightBlocks;
+        if (blocks > most) blocks = most;
+        const size_t smem = weights_smem<D, T>(blocks);
+        const dim3 grid(148 * (smem <= 56 * 1024 ? 4 : smem <= 74 * 1024 ? 3 : 2));
         const cudaError_t e =
-            chunk ? kv4_launch(kv4_weights_kernel<D, T, true>, dim3(kGridMax), kAttendThreads,
-                               weights_smem<D, T>(blocks), s, c, qv, sc, maps, r, blocks)
-                  : kv4_launch(kv4_weights_kernel<D, T, false>, dim3(kGridMax), kAttendThreads,
-                               weights_smem<D, T>(blocks), s, c, qv, sc, maps, r, blocks);
+            chunk ? kv4_launch(kv4_weights_kernel<D, T, true>, grid, kAttendThreads, smem, s, c, qv, sc,
+                               maps, r, blocks)
+                  : kv4_launch(kv4_weights_kernel<D, T, false>, grid, kAttendThreads, smem, s, c, qv, sc,
+                               maps, r, blocks);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
