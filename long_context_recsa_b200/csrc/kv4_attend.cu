@@ -750,7 +750,8 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         auto slot = [&](int64_t cta) { return 2 * cta + (cta == cta0 ? 1 : 0); };
         auto part_of = [&](int64_t cta) { return sc_.part + (size_t)slot(cta) * RB * (D + 2); };
         float* part = whole ? nullptr : part_of(blockIdx.x);
-        for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
+        const int nr = row_end - row0 < RB ? row_end - row0 : RB;   // rows of the block that are there
+        for (int i = threadIdx.x; i < nr * (D / 4); i += kAttendThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
             float mx = red_m[0][r];
 #pragma unroll
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                 }
                 __syncthreads();
                 float* to = part_of(first);
-                for (int i = threadIdx.x; i < RB * (D / 4); i += kAttendThreads) {
+                for (int i = threadIdx.x; i < nr * (D / 4); i += kAttendThreads) {
                     const int r = i / (D / 4), d4 = i % (D / 4);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -886,7 +887,12 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     __syncthreads();
     const int64_t total = pl.pre[c.B];
     int64_t quota = (total + gridDim.x - 1) / gridDim.x;
-    if (quota < kAttendWarps) quota = kAttendWarps;
+    // few tiles: a CTA's warps share a tile's blocks of rows instead of taking a tile each
+    const bool spread = n_blocks >= kAttendWarps && quota <= 2;
+    if (!spread && quota < kAttendWarps) quota = kAttendWarps;
+    const int step = spread ? 1 : kAttendWarps, base = spread ? 0 : warp;
+    const int k_step = spread ? kAttendWarps : 1, k_base = spread ? warp : 0;
+    __shared__ float sums[kAttendWarps][kTile];
     int64_t at = blockIdx.x * quota;
     const int64_t at_end = at + quota < total ? at + quota : total;
     uint32_t phase = 0;
@@ -919,9 +925,9 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
             bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
             if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
         };
-        int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - warp + kAttendWarps - 1) / kAttendWarps : 0;
+        int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - base + step - 1) / step : 0;
         if (lane == 0 && alive)
-            for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + warp + s * kAttendWarps, s);
+            for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + base + s * step, s);
         if (row0 < row_end) {
             stage_rows<D, T, 1>(rs, n_blocks, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp,
                                 kAttendWarps, lane);
@@ -932,17 +938,16 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         __syncthreads();
         for (int it = 0; it < mine; ++it) {
             const int s = it % kStagesKv4;
-            const int tile = tile0 + warp + it * kAttendWarps;
-            if (!alive) break;
-            if (!__all_sync(kFull, mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status))) {
+            const int tile = tile0 + base + it * step;
+            if (alive && __all_sync(kFull, mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status)))
+                phase ^= 1u << s;
+            else
                 alive = false;
-                break;
-            }
-            phase ^= 1u << s;
+            if (!alive && !spread) break;      // (warps that share a tile meet below)
             const unsigned char* st = my_ring + s * St::kBytes;
             const uint32_t sa = smem_u32(st);
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < 2 && alive; ++half) {
                 const int r0 = half * 16;
                 const int64_t tok = (int64_t)tile * kTile + r0 + g;
                 if (tok - g >= L) break;
@@ -953,7 +958,7 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                 }
                 float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll 1
-                for (int k = 0; k < n_blocks; ++k) {
+                for (int k = k_base; k < n_blocks; k += k_step) {
                     if (row0 + k * RB >= row_end) break;
                     uint4 qreg[NG];
                     float qsum[RL][NG];
@@ -979,7 +984,10 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                 sum1 += __shfl_xor_sync(kFull, sum1, 1);
                 sum0 += __shfl_xor_sync(kFull, sum0, 2);
                 sum1 += __shfl_xor_sync(kFull, sum1, 2);
-                if (t == 0) {
+                if (t == 0 && spread) {
+                    sums[warp][r0 + g] = sum0;
+                    sums[warp][r0 + g + 8] = sum1;
+                } else if (t == 0) {
                     // this warp's alone: what the tile brought, and more
                     const float* old = reinterpret_cast<const float*>(st + St::kW) + r0 + g;
                     float* w = c.w + u * c.R + tok;
@@ -987,9 +995,20 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                     if (tok + 8 < L) w[8] = old[8] + sum1;
                 }
             }
+            if (spread) {
+                __syncthreads();
+                const int64_t tok = (int64_t)tile * kTile + lane;
+                if (warp == 0 && alive && tok < L) {
+                    float x = reinterpret_cast<const float*>(st + St::kW)[lane];
+#pragma unroll
+                    for (int i = 0; i < kAttendWarps; ++i) x += sums[i][lane];
+                    c.w[u * c.R + tok] = x;
+                }
+                __syncthreads();
+            }
             __syncwarp();
-            if (lane == 0 && it + kStagesKv4 < mine)
-                fetch(tile0 + warp + (it + kStagesKv4) * kAttendWarps, s);
+            if (lane == 0 && alive && it + kStagesKv4 < mine)
+                fetch(tile0 + base + (it + kStagesKv4) * step, s);
         }
         if (!alive) {
             for (int s = 0; s < kStagesKv4; ++s)
