@@ -87,8 +87,9 @@ size_t kv4_chunk_part_floats(int D, int rows);          // the same for kv4_laun
 cudaError_t kv4_prepare_chunk(int D);
 // bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows
 cudaError_t kv4_launch_chunk(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s);
+// renorm: after kv4_launch_chunk, whose row sums are good to 2e-6, not to fp32
 cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s);
+                               const Kv4Maps& maps, int chunk, int renorm, int dtype, cudaStream_t s);
 
 // A launch that may start while the previous kernel of the stream finishes (every
 // kernel of the cache passes pdl_wait() in all its threads before it touches memory).

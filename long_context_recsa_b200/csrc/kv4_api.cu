@@ -291,7 +291,7 @@ recsa_status recsa_kv4_decode(recsa_kv4* t, const void* q, void* out, int32_t ac
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = kv4_launch_attend(t->c, qv, t->sc, t->maps, 0, t->cfg.dtype, s);
     if (e == cudaSuccess && accumulate)
-        e = kv4_launch_weights(t->c, qv, t->sc, t->maps, 0, t->cfg.dtype, s);
+        e = kv4_launch_weights(t->c, qv, t->sc, t->maps, 0, 0, t->cfg.dtype, s);
     return done(e);
 }
 
@@ -313,12 +313,12 @@ recsa_status recsa_kv4_prefill_chunk(recsa_kv4* t, const void* Q, int32_t n, con
         qv.i0 = i0;
         qv.w = n - i0 < wave ? n - i0 : wave;
         qv.acc_rows = accumulate_rows < n ? accumulate_rows : n;
-        e = chunk_on_tensor_cores(t->cfg.dtype, qv.w * t->c.G)
-                ? kv4_launch_chunk(t->c, qv, t->sc, s)
-                : kv4_launch_attend(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);
+        const bool tc = chunk_on_tensor_cores(t->cfg.dtype, qv.w * t->c.G);
+        e = tc ? kv4_launch_chunk(t->c, qv, t->sc, s)
+               : kv4_launch_attend(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);
         // with counts the newest rows may lie in any wave, else in the last ones
         if (e == cudaSuccess && qv.acc_rows > 0 && (counts || i0 + qv.w > n - qv.acc_rows))
-            e = kv4_launch_weights(t->c, qv, t->sc, t->maps, 1, t->cfg.dtype, s);
+            e = kv4_launch_weights(t->c, qv, t->sc, t->maps, 1, tc, t->cfg.dtype, s);
     }
     return done(e);
 }

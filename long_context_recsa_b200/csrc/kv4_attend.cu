@@ -857,13 +857,17 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 
 // Accumulated weights: w[slot] += sum over the newest acc_rows rows of every sequence
 // (all G heads) of exp2(score - lse), with the scores formed again from the keys as above
-// and the rows' lse from the attention launch before it.  Rows rb0 * RB .. of the rows
-// that count, up to NP blocks a launch, are held in shared memory; a tile's codes are
-// read once for all of them.  Every slot belongs to one warp, so sums have one order.
-template <int D, int T, bool CHUNK>
+// and the rows' lse from the attention launch before it.  The rows that count are held in
+// shared memory, as many as fit a launch; a tile's codes are read once for all of them.
+// Every slot belongs to one warp (or one CTA), so sums have one order.
+//
+// After the chunk kernel the lse come from keys rounded to fp16, which would leave 2e-6 in the
+// weights.  There a launch with SUMS goes first: it adds exp2(score - lse) by rows, which
+// gives 1 but for that error, and the second launch takes its logarithm off (`renorm`).
+template <int D, int T, bool CHUNK, bool SUMS>
 __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,
-    int n_blocks) {
+    int n_blocks, int renorm) {
     constexpr int NG = D / kKv4Group, RB = 8 / T, RL = 2 / T;
     using St = Stage<D>;
     using RowsT = Rows<D, T, 1>;
@@ -873,6 +877,7 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     unsigned char* ring = smem;
     RowsT* rs = reinterpret_cast<RowsT*>(smem + kAttendWarps * kStagesKv4 * St::kBytes);
     float* lse = reinterpret_cast<float*>(rs + n_blocks);   // [n_blocks][RB]
+    float* row_sums = lse + n_blocks * RB;                  // SUMS: [warp][n_blocks][RB]
     __shared__ Plan pl;
     __shared__ uint64_t bars[kAttendWarps][kStagesKv4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -919,9 +924,9 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
             unsigned char* st = my_ring + s * St::kBytes;
             uint64_t* bar = &bars[warp][s];
             const int64_t r = (int64_t)tile * kTile;
-            mbar_expect_tx(bar, St::kCodes + St::kPars + (CHUNK ? 2 : 1) * kTile * 4);
+            mbar_expect_tx(bar, St::kCodes + St::kPars + ((CHUNK ? 1 : 0) + (SUMS ? 0 : 1)) * kTile * 4);
             tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
-            bulk_g2s(st + St::kW, c.w + u * c.R + r, kTile * 4, bar);
+            if (!SUMS) bulk_g2s(st + St::kW, c.w + u * c.R + r, kTile * 4, bar);
             bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
             if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
         };
@@ -931,9 +936,23 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         if (row0 < row_end) {
             stage_rows<D, T, 1>(rs, n_blocks, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp,
                                 kAttendWarps, lane);
-            for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads)
-                lse[i] = row0 + i < row_end
+            const int64_t unit0 = at - tile0;
+            const int64_t cta0 = unit0 / quota, cta1 = (unit0 + tiles - 1) / quota;
+            for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads) {
+                float x = row0 + i < row_end
                     ? sc_.lse[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G] : INFINITY;
+                if (!SUMS && renorm && row0 + i < row_end) {
+                    float sum = 0.0f;
+#pragma unroll 4
+                    for (int64_t k = cta0; k <= cta1; ++k)
+                        sum += __ldcg(sc_.part + (2 * k + (k == cta0 ? 1 : 0)) * n_blocks * RB + i);
+                    if (sum != 0.0f) x += log2f(sum);
+                }
+                lse[i] = x;
+            }
+            if (SUMS)
+                for (int i = threadIdx.x; i < kAttendWarps * n_blocks * RB; i += kAttendThreads)
+                    row_sums[i] = 0.0f;
         }
         __syncthreads();
         for (int it = 0; it < mine; ++it) {
@@ -976,10 +995,19 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                         const int lm = rs[k].lim[t * RL + e];
                         const float x0 = ex2(sc[0][2 * e] * f - ls), x1 = ex2(sc[0][2 * e + 1] * f - ls);
                         // rows that are not there have lm = -1, below every position
-                        if ((CHUNK ? pos0 : 0) <= lm) sum0 += x0;
-                        if ((CHUNK ? pos1 : 0) <= lm) sum1 += x1;
+                        if constexpr (SUMS) {
+                            float x = (pos0 <= lm && tok < L ? x0 : 0.0f) + (pos1 <= lm && tok + 8 < L ? x1 : 0.0f);
+                            x += __shfl_xor_sync(kFull, x, 4);
+                            x += __shfl_xor_sync(kFull, x, 8);
+                            x += __shfl_xor_sync(kFull, x, 16);
+                            if (g == 0) row_sums[(warp * n_blocks + k) * RB + t * RL + e] += x;
+                        } else {
+                            if ((CHUNK ? pos0 : 0) <= lm) sum0 += x0;
+                            if ((CHUNK ? pos1 : 0) <= lm) sum1 += x1;
+                        }
                     }
                 }
+                if constexpr (SUMS) continue;
                 sum0 += __shfl_xor_sync(kFull, sum0, 1);
                 sum1 += __shfl_xor_sync(kFull, sum1, 1);
                 sum0 += __shfl_xor_sync(kFull, sum0, 2);
@@ -995,7 +1023,7 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                     if (tok + 8 < L) w[8] = old[8] + sum1;
                 }
             }
-            if (spread) {
+            if (spread && !SUMS) {
                 __syncthreads();
                 const int64_t tok = (int64_t)tile * kTile + lane;
                 if (warp == 0 && alive && tok < L) {
@@ -1014,6 +1042,16 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
             for (int s = 0; s < kStagesKv4; ++s)
                 if (lane == 0) mbar_wait_bounded(&bars[warp][s], (phase >> s) & 1u, c.status, kWaitPollsAfterFail);
         }
+        if constexpr (SUMS) {
+            __syncthreads();
+            if (row0 < row_end)
+                for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads) {
+                    float x = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kAttendWarps; ++k) x += row_sums[k * n_blocks * RB + i];
+                    sc_.part[(2 * (int64_t)blockIdx.x + (tile0 == 0 ? 1 : 0)) * n_blocks * RB + i] = x;
+                }
+        }
         at += tile1 - tile0;
         __syncthreads();
     }
@@ -1031,13 +1069,13 @@ constexpr size_t attend_smem() {
 template <int D, int T>
 constexpr size_t weights_smem(int blocks) {
     return 1024 + (size_t)kAttendWarps * kStagesKv4 * Stage<D>::kBytes +
-           (size_t)blocks * (sizeof(Rows<D, T, 1>) + sizeof(float) * 8 / T);
+           (size_t)blocks * (sizeof(Rows<D, T, 1>) + (1 + kAttendWarps) * sizeof(float) * 8 / T);
 }
 // Column sets a weights launch holds: 64 KB of rows, so that two CTAs share an SM beside
 // their rings (four with half of it).
 template <int D, int T>
 constexpr int weight_blocks() {
-    return 65536 / (int)(sizeof(Rows<D, T, 1>) + sizeof(float) * 8 / T);
+    return 65536 / (int)(sizeof(Rows<D, T, 1>) + (1 + kAttendWarps) * sizeof(float) * 8 / T);
 }
 
 // Column sets of a block: the fewest that hold the rows, up to four (the accumulators of
@@ -1062,8 +1100,11 @@ cudaError_t prepare_impl() {
         if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 2, true>, attend_smem<D, T, 2>());
         if (e == cudaSuccess) e = allow(kv4_attend_kernel<D, T, 4, true>, attend_smem<D, T, 4>());
     }
-    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false>, weights_smem<D, T>(weight_blocks<D, T>()));
-    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true>, weights_smem<D, T>(weight_blocks<D, T>()));
+    const size_t most = weights_smem<D, T>(weight_blocks<D, T>());
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, false, false>, most);
+    if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true, false>, most);
+    if constexpr (T == 1)
+        if (e == cudaSuccess) e = allow(kv4_weights_kernel<D, T, true, true>, most);
     return e;
 }
 
@@ -1097,7 +1138,7 @@ cudaError_t attend_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& 
 
 template <int D, int T>
 cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                         const Kv4Maps& maps, int chunk, cudaStream_t s) {
+                         const Kv4Maps& maps, int chunk, int renorm, cudaStream_t s) {
     const int rows = (qv.acc_rows < qv.w ? qv.acc_rows : qv.w) * c.G, per = 8 / T;
     constexpr int most = weight_blocks<D, T>();
     for (int r = 0; r < rows; r += most * per) {
@@ -1105,11 +1146,16 @@ cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch&
         if (blocks > most) blocks = most;
         const size_t smem = weights_smem<D, T>(blocks);
         const dim3 grid(148 * (smem <= 56 * 1024 ? 4 : smem <= 74 * 1024 ? 3 : 2));
-        const cudaError_t e =
-            chunk ? kv4_launch(kv4_weights_kernel<D, T, true>, grid, kAttendThreads, smem, s, c, qv, sc,
-                               maps, r, blocks)
-                  : kv4_launch(kv4_weights_kernel<D, T, false>, grid, kAttendThreads, smem, s, c, qv, sc,
-                               maps, r, blocks);
+        cudaError_t e = cudaSuccess;
+        if constexpr (T == 1)
+            if (renorm)
+                e = kv4_launch(kv4_weights_kernel<D, T, true, true>, grid, kAttendThreads, smem, s, c, qv,
+                               sc, maps, r, blocks, 0);
+        if (e != cudaSuccess) return e;
+        e = chunk ? kv4_launch(kv4_weights_kernel<D, T, true, false>, grid, kAttendThreads, smem, s, c, qv,
+                               sc, maps, r, blocks, renorm)
+                  : kv4_launch(kv4_weights_kernel<D, T, false, false>, grid, kAttendThreads, smem, s, c,
+                               qv, sc, maps, r, blocks, 0);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1139,10 +1185,10 @@ cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scr
 }
 
 cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s) {
+                               const Kv4Maps& maps, int chunk, int renorm, int dtype, cudaStream_t s) {
     NvtxRange nv("recsa kv4 weights");
     const int D_ = c.D;
-    KV4_ATTEND(weights_impl, c, qv, sc, maps, chunk, s);
+    KV4_ATTEND(weights_impl, c, qv, sc, maps, chunk, renorm, s);
 }
 
 }  // namespace recsa
