@@ -933,6 +933,7 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - base + step - 1) / step : 0;
         if (lane == 0 && alive)
             for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + base + s * step, s);
+        const int left = (row_end - row0 + RB - 1) / RB, live_blocks = left < n_blocks ? left : n_blocks;
         if (row0 < row_end) {
             stage_rows<D, T, 1>(rs, n_blocks, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp,
                                 kAttendWarps, lane);
@@ -976,9 +977,9 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                     pos1 = *reinterpret_cast<const int*>(st + St::kPos + (r0 + g + 8) * 4);
                 }
                 float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll 1
-                for (int k = k_base; k < n_blocks; k += k_step) {
-                    if (row0 + k * RB >= row_end) break;
+                // several blocks side by side: one alone is a chain of latencies
+#pragma unroll 4
+                for (int k = k_base; k < live_blocks; k += k_step) {
                     uint4 qreg[NG];
                     float qsum[RL][NG];
 #pragma unroll
