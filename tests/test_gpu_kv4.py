@@ -367,6 +367,35 @@ def test_nan_tokens_reach_only_the_rows_that_see_them(R, dtype, d):
     assert torch.isfinite(kv4.decode(Q[:, 0].contiguous().cuda())).all()
 
 
+@pytest.mark.parametrize("big", [1.0, 2.0 ** 10, 2.0 ** 28])
+@pytest.mark.parametrize("n,G", [(5, 1), (20, 2), (70, 4)])
+def test_chunk_of_large_and_growing_logits(R, n, G, big):
+    """Scores that rise along the cache, so that the running reference moves in every tile, up
+    to 2^35.  Five neighbouring keys are equal, in every rounding; the next five score 2 * big
+    less.  With big = 1 the general bound holds.  With the larger ones all weight of a row lies
+    on the newest keys it sees that are equal (exp(-2048) = 0), whatever the keys' rounding;
+    P and V are off by 2^-11 each."""
+    d, L = 64, 600
+    k = torch.zeros(1, 1, L, d)
+    k[0, 0, :, 0] = torch.arange(L).float() // 5 - 60    # |k| <= 60: 8 bits; lo = s = exact or 0
+    v = rand((1, 1, L, d), 4, "bf16").float()
+    Q = torch.zeros(1, n, G, d)
+    Q[..., 0] = 16.0 * big                               # score = 2 big k
+    cfg = R.Config(head_dim=d, n_q_heads=G, n_kv_heads=1, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, L, 1, max_queries=n)
+    kv4.recsa_kv4_build(k.bfloat16().cuda(), v.bfloat16().cuda(), [L])
+    u = O.Unit(d)
+    u.append(np64(k.bfloat16()[0, 0]), np64(v.bfloat16()[0, 0]))
+    out = np64(kv4.prefill(Q.bfloat16().cuda())[0])
+    for i in range(n):
+        qs = np64(Q[0, i, :1])
+        want = u.attend(qs, L - n + i)
+        tc = on_tensor_cores("bf16", n * G)
+        floor = bound_of(u, qs, "bf16", tc)[1] if big == 1 else 2.0 ** -10 * np.abs(u.v).max()
+        check_rows(torch.from_numpy(out[i]), np.repeat(want, G, 0), floor, "bf16", i)
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
 # ------------------------------------------------------------------------- eviction ----
 def set_weights(kv4, units, seed, ties=False):
     g = torch.Generator().manual_seed(seed)
@@ -392,7 +421,8 @@ def check_evicted(kv4, units, dtype):
 @pytest.mark.parametrize("dtype,d,lengths,budget,first,recent", [
     ("bf16", 128, [100, 30, 31], 30, 4, 8), ("f32", 64, [2000, 0, 1999], 1000, 0, 0),
     ("bf16", 64, [5000], 64, 32, 32), ("f32", 128, [3, 1, 2], 1, 1, 0), ("bf16", 128, [1500, 9], 1499, 0, 700),
-    ("f32", 64, [1025], 1, 0, 1)])
+    ("f32", 64, [1025], 1, 0, 1), ("bf16", 64, [9000, 7000, 50], 4000, 16, 100), ("f32", 64, [6500], 6400, 0, 0),
+    ("bf16", 128, [8193], 17, 3, 9)])
 def test_evict(R, dtype, d, lengths, budget, first, recent, ties):
     kv4, units = make(R, dtype, d, 2, 1, lengths, extra=8)
     set_weights(kv4, units, 4, ties)
@@ -404,6 +434,40 @@ def test_evict(R, dtype, d, lengths, budget, first, recent, ties):
     q = rand((len(lengths), 2, d), 8, dtype)
     check_decode(kv4, units, q, kv4.decode(q.cuda()), dtype, 1)
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+def test_evict_short_length_in_a_large_cache(R):
+    """Most CTAs of the cluster own no slot."""
+    kv4, units = make(R, "f32", 64, 2, 1, [100, 129, 1], cap=20000)
+    set_weights(kv4, units, 5)
+    kv4.recsa_kv4_evict(50, 3, 7)
+    for row in units:
+        for u in row:
+            u.evict(50, 3, 7)
+    check_evicted(kv4, units, "f32")
+
+
+def test_evict_past_the_keys_that_shared_memory_holds(R):
+    L, budget = 400_000, 150_000
+    cfg = R.Config(head_dim=64, n_q_heads=1, n_kv_heads=1, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, L + 7, 1)
+    g = torch.Generator().manual_seed(1)
+    x = torch.zeros(1, 1, L, 64, dtype=torch.bfloat16, device="cuda")
+    kv4.recsa_kv4_build(x, x, [L])
+    w = (torch.rand(L, generator=g) * 1000).floor()      # many ties
+    kv4.weights()[0, 0, :L] = w.cuda()
+    kv4.recsa_kv4_evict(budget, 5, 1000)
+    safe = torch.zeros(L, dtype=torch.bool)
+    safe[:5] = safe[L - 1000:] = True
+    key = torch.where(safe, torch.tensor(float("inf")), w)
+    keep = torch.sort(key, descending=True, stable=True).indices[:budget]
+    kept = torch.zeros(L, dtype=torch.bool)
+    kept[keep] = True
+    want = torch.arange(budget)
+    want[~kept[:budget]] = torch.arange(budget, L)[kept[budget:]]
+    assert torch.equal(kv4.positions()[0, 0, :budget].cpu().long(), want)
+    assert torch.equal(kv4.weights()[0, 0, :budget].cpu(), w[want])
+    assert (kv4.weights()[0, 0, budget:] == 0).all() and kv4.lengths().tolist() == [budget]
 
 
 def test_evict_orders_odd_weights(R):
