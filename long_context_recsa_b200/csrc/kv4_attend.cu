@@ -35,6 +35,12 @@
 // of TMA stages, running maximum and accumulators, and meet only at the end of a unit.  A
 // unit cut over several CTAs is joined by the last of each 16 and then by the last of those
 // (one CTA joining all 74 of a unit took longer than the unit).
+//
+// Measured (B200): decode of 4 x 524288 tokens, 8 KV heads, 32 heads, d = 128: 671 us for
+// 2684 MB, 4.0 TB/s, 61% of a plain copy's rate.  Instructions bound it: 480 a warp for 16
+// tokens of K and V, issued in 60% of the cycles, half of them on the pipe of the masks and
+// conversions.  131072 tokens of one sequence: 64 us, of which the start, the plan and the
+// joins are about 20.
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -864,6 +870,10 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 // After the chunk kernel the lse come from keys rounded to fp16, which would leave 2e-6 in the
 // weights.  There a launch with SUMS goes first: it adds exp2(score - lse) by rows, which
 // gives 1 but for that error, and the second launch takes its logarithm off (`renorm`).
+//
+// Measured: 32 us for one row of 131072 tokens x 8 KV heads (84 MB of keys, 8 of weights);
+// 128 rows a KV head of 16384 x 8: 88 us a launch, bound by the latency of scores and
+// exponentials at eight warps an SM.
 template <int D, int T, bool CHUNK, bool SUMS>
 __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,
