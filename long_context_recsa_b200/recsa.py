@@ -473,7 +473,7 @@ class RecsaKV4:
                                    self._on(stream)), "recsa_kv4_build")
 
     def recsa_kv4_append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts=None, stream=None):
-        n = k_new.shape[2]
+        n = k_new.shape[2] if k_new.dim() == 4 else 0
         shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
         _check(lib.recsa_kv4_append(self.handle, self._rows(k_new, shape, "k_new"),
                                     self._rows(v_new, shape, "v_new"), n, self._counts(counts),
@@ -488,7 +488,7 @@ class RecsaKV4:
 
     def recsa_kv4_prefill_chunk(self, Q: torch.Tensor, O: torch.Tensor, counts=None,
                                 accumulate_rows: int = 0, stream=None):
-        n = Q.shape[1]
+        n = Q.shape[1] if Q.dim() == 4 else 0
         shape = (self.batch, n, self.cfg.n_q_heads, self.cfg.head_dim)
         _check(lib.recsa_kv4_prefill_chunk(self.handle, self._rows(Q, shape, "Q"), n,
                                            self._counts(counts), self._rows(O, shape, "O"),

@@ -596,6 +596,52 @@ def test_captured_step_replays(R):
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK
 
 
+@pytest.mark.parametrize("G,n", [(4, 40), (2, 3)])
+def test_captured_chunk_replays_after_eager_calls(R, G, n):
+    """A chunk with weights, captured while an eager chunk of the same handle came before and
+    comes between replays; the tensor-core form and the other."""
+    d, B, Hkv = 128, 2, 2
+    kv4, _ = make(R, "bf16", d, Hkv, G, [300, 90], max_queries=B * n)
+    Qs = [rand((B, n, G * Hkv, d), 70 + i, "bf16").cuda() for i in range(3)]
+    want = [kv4.prefill(q) for q in Qs]
+    kv4.prefill(Qs[0], accumulate_rows=2)
+    once = kv4.weights().clone()
+    Q, O_ = Qs[0].clone(), torch.empty_like(Qs[0])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            kv4.recsa_kv4_prefill_chunk(Q, O_, accumulate_rows=2)
+    for i in range(3):
+        Q.copy_(Qs[i])
+        kv4.weights().zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O_, want[i]), i
+        assert i > 0 or torch.equal(kv4.weights(), once)
+        assert torch.equal(kv4.prefill(Qs[2]), want[2])
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+def test_two_chunks_on_two_streams(R):
+    """Two caches' tensor-core chunks at once (each takes an SM's whole TMEM)."""
+    n, G = 40, 4
+    a, _ = make(R, "bf16", 128, 2, G, [900, 64], max_queries=2 * n)
+    b, _ = make(R, "bf16", 64, 2, G, [500, 1200], max_queries=2 * n)
+    qa, qb = rand((2, n, 8, 128), 1, "bf16").cuda(), rand((2, n, 8, 64), 2, "bf16").cuda()
+    want_a, want_b = a.prefill(qa), b.prefill(qb)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    oa, ob = [torch.empty_like(qa) for _ in range(10)], [torch.empty_like(qb) for _ in range(10)]
+    for i in range(10):
+        a.recsa_kv4_prefill_chunk(qa, oa[i], stream=s1)
+        b.recsa_kv4_prefill_chunk(qb, ob[i], stream=s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want_a) for x in oa) and all(torch.equal(x, want_b) for x in ob)
+    assert a.recsa_kv4_get_status() == R.RECSA_OK and b.recsa_kv4_get_status() == R.RECSA_OK
+
+
 def test_two_caches_on_two_streams(R):
     """Handles do not share state: concurrent steps on two streams equal serial ones."""
     a, ua = make(R, "bf16", 128, 2, 4, [900, 33])
@@ -629,6 +675,13 @@ def test_binding_refuses_wrong_tensors(R):
         kv4.recsa_kv4_build(k, k, [-1, 4])
     with pytest.raises(ValueError):
         kv4.recsa_kv4_append(k, k, torch.tensor([1, 1], device="cuda"))      # int64 counts
+    for flat in (k[0], k[0, 0, 0]):
+        with pytest.raises(ValueError):
+            kv4.recsa_kv4_append(flat, flat)
+        with pytest.raises(ValueError):
+            kv4.recsa_kv4_prefill_chunk(flat, flat.clone())
+    with pytest.raises(R.RecsaError):
+        kv4.recsa_kv4_append(k[:, :, :0], k[:, :, :0])   # no rows
     with pytest.raises(R.RecsaError):
         kv4.read(15, 6)                                  # past the capacity
     with pytest.raises(R.RecsaError):
