@@ -680,29 +680,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                         nanbits |= nan_groups<NG>(pos_s[slot], nan_any[slot], nan_s[slot], lim);
                     // P is formed with the old reference; should one pass kMostP, that
                     // moves and the 32 scores are read once more (then none can pass it)
-                    bool moved = false;
+                    auto move_to = [&](int k, bool over) {
+                        const float f = grow(ts, k, rsc, over, ref);
+                        l2.x *= f;
+                        l2.y *= f;
+                        // the products before S are done (one thread issued both, and the
+                        // barrier stands for all it had issued)
+                        if (j > 0) rescale_o<D>(to, f);
+                    };
 #pragma unroll 1
-                    for (int k = 0; k < kTok / 32;) {
-                        float v[32];
+                    for (int k = 0; k < kTok / 32; k += 2) {
+                        // 64 scores at a time; what a retry needs is read again, so that
+                        // nothing of them is held over the call
+                        float a[32], z[32];
                         uint32_t p[16];
                         float2 sum;
-                        ld32(ts + k * 32, v);
-                        ld_done(v);
-                        const bool over = form_p(v, rsc, ref, p, sum) > kMostP;
-                        if (__any_sync(kFull, over) && !moved) {
-                            const float f = grow(ts, k, rsc, over, ref);
-                            l2.x *= f;
-                            l2.y *= f;
-                            // the products before S are done (one thread issued both, and
-                            // the barrier stands for all it had issued)
-                            if (j > 0) rescale_o<D>(to, f);
-                            moved = true;
-                            continue;
+                        ld32(ts + k * 32, a);
+                        ld32(ts + k * 32 + 32, z);
+                        ld_done(a);
+                        ld_done(z);
+                        bool over = form_p(a, rsc, ref, p, sum) > kMostP;
+                        if (__any_sync(kFull, over)) {
+                            move_to(k, over);
+                            ld32(ts + k * 32, a);
+                            ld32(ts + k * 32 + 32, z);
+                            ld_done(a);
+                            ld_done(z);
+                            form_p(a, rsc, ref, p, sum);
                         }
-                        moved = false;
                         l2 = add2(l2, sum);
                         st16(ts + k * 16, p);
-                        ++k;
+                        over = form_p(z, rsc, ref, p, sum) > kMostP;
+                        if (__any_sync(kFull, over)) {
+                            move_to(k + 1, over);
+                            ld32(ts + k * 32 + 32, z);
+                            ld_done(z);
+                            form_p(z, rsc, ref, p, sum);
+                        }
+                        l2 = add2(l2, sum);
+                        st16(ts + k * 16 + 16, p);
                     }
                     st_done();
                 }
