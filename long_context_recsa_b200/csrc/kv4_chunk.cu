@@ -270,20 +270,6 @@ __device__ __forceinline__ void ld16(uint32_t t, uint32_t (&u)[16]) {
         : "r"(t)
         : "memory");
 }
-// When the running maximum moves: the row's sums so far, by f <= 1.
-template <int D>
-__device__ __noinline__ void rescale_o(uint32_t t, float f) {
-#pragma unroll 1
-    for (int k = 0; k < D; k += 32) {
-        float o[32];
-        ld32(t + k, o);
-        ld_done(o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= f;
-        st32(t + k, o);
-    }
-    st_done();
-}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 y;
@@ -350,9 +336,14 @@ __device__ __forceinline__ float form_p(const float (&s)[32], float scale, float
     sum = add2(l[0], l[1]);
     return fmaxf(most[0], most[1]);
 }
-// Moves the reference of the rows that are `over` to the largest of scores 32 k .. 32 k + 31;
-// the sixteens of P that the tile already has are scaled by the factor, which is returned.
-__device__ __noinline__ float grow(uint32_t ts, int k, float rsc, bool over, float& ref) {
+// Moves the reference of the rows that are `over` to the largest of scores 32 k .. 32 k + 31:
+// the sixteens of P that the tile already has, O (where products went into it) and the sum
+// are scaled by the factor, and P of these scores is formed and stored.  The products before
+// S are done by now: one thread issued both, and S's barrier stands for all it had issued.
+struct Moved { float ref, l; };
+template <int D>
+__device__ __noinline__ Moved move_reference(uint32_t ts, uint32_t to, int k, bool has_o, float rsc,
+                                             bool over, float ref, float2 l2) {
     float s[32];
     ld32(ts + k * 32, s);
     ld_done(s);
@@ -375,7 +366,20 @@ __device__ __noinline__ float grow(uint32_t ts, int k, float rsc, bool over, flo
         for (int e = 0; e < 16; ++e) p[e] = as_u(__hmul2(as_h2(p[e]), h));
         st16(ts + i * 16, p);
     }
-    return f;
+    uint32_t p[16];
+    float2 sum;
+    form_p(s, rsc, ref, p, sum);
+    st16(ts + k * 16, p);
+#pragma unroll 1
+    for (int i = 0; has_o && i < D; i += 32) {
+        ld32(to + i, s);
+        ld_done(s);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] *= f;
+        st32(to + i, s);
+    }
+    st_done();
+    return {ref, fmaf(l2.x + l2.y, f, sum.x + sum.y)};
 }
 // Groups of dims in which a token that the row sees holds NaN.
 template <int NG>
@@ -678,20 +682,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     if (__any_sync(kFull, most > lim && lim >= 0)) hide_scores(ts, pos_s[slot], lim);
                     if (na.x | na.y | na.z | na.w)
                         nanbits |= nan_groups<NG>(pos_s[slot], nan_any[slot], nan_s[slot], lim);
-                    // P is formed with the old reference; should one pass kMostP, that
-                    // moves and the 32 scores are read once more (then none can pass it)
-                    auto move_to = [&](int k, bool over) {
-                        const float f = grow(ts, k, rsc, over, ref);
-                        l2.x *= f;
-                        l2.y *= f;
-                        // the products before S are done (one thread issued both, and the
-                        // barrier stands for all it had issued)
-                        if (j > 0) rescale_o<D>(to, f);
-                    };
+                    // P is formed with the old reference; should one pass kMostP, that moves to
+                    // the largest of the 32 (then none can pass it)
 #pragma unroll 1
                     for (int k = 0; k < kTok / 32; k += 2) {
-                        // 64 scores at a time; what a retry needs is read again, so that
-                        // nothing of them is held over the call
+                        // 64 scores at a time; after a retry (a call, which does the 32 scores
+                        // itself) the others are read again, so that nothing is held over it
                         float a[32], z[32];
                         uint32_t p[16];
                         float2 sum;
@@ -701,24 +697,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                         ld_done(z);
                         bool over = form_p(a, rsc, ref, p, sum) > kMostP;
                         if (__any_sync(kFull, over)) {
-                            move_to(k, over);
-                            ld32(ts + k * 32, a);
+                            const Moved to_new = move_reference<D>(ts, to, k, j > 0, rsc, over, ref, l2);
+                            ref = to_new.ref;
+                            l2 = make_float2(to_new.l, 0.0f);
                             ld32(ts + k * 32 + 32, z);
-                            ld_done(a);
                             ld_done(z);
-                            form_p(a, rsc, ref, p, sum);
+                        } else {
+                            l2 = add2(l2, sum);
+                            st16(ts + k * 16, p);
                         }
-                        l2 = add2(l2, sum);
-                        st16(ts + k * 16, p);
                         over = form_p(z, rsc, ref, p, sum) > kMostP;
                         if (__any_sync(kFull, over)) {
-                            move_to(k + 1, over);
-                            ld32(ts + k * 32 + 32, z);
-                            ld_done(z);
-                            form_p(z, rsc, ref, p, sum);
+                            const Moved to_new = move_reference<D>(ts, to, k + 1, j > 0, rsc, over, ref, l2);
+                            ref = to_new.ref;
+                            l2 = make_float2(to_new.l, 0.0f);
+                        } else {
+                            l2 = add2(l2, sum);
+                            st16(ts + k * 16 + 16, p);
                         }
-                        l2 = add2(l2, sum);
-                        st16(ts + k * 16 + 16, p);
                     }
                     st_done();
                 }
