@@ -36,8 +36,8 @@
 // unit cut over several CTAs is joined by the last of each 16 and then by the last of those
 // (one CTA joining all 74 of a unit took longer than the unit).
 //
-// Measured (B200): decode of 4 x 524288 tokens, 8 KV heads, 32 heads, d = 128: 671 us for
-// 2684 MB, 4.0 TB/s, 61% of a plain copy's rate.  Instructions bound it: 480 a warp for 16
+// Measured (B200): decode of 4 x 524288 tokens, 8 KV heads, 32 heads, d = 128: 666 us for
+// 2684 MB, 4.0 TB/s, 62% of a plain copy's rate.  Instructions bound it: 480 a warp for 16
 // tokens of K and V, issued in 60% of the cycles, half of them on the pipe of the masks and
 // conversions.  131072 tokens of one sequence: 64 us, of which the start, the plan and the
 // joins are about 20.

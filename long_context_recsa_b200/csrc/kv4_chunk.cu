@@ -21,15 +21,15 @@
 //
 // Bound: 4 d flops a pair of row and token.  A tile of 128 tokens and two streams takes 2048
 // cycles of products at the tensor cores' rate and as many of exponentials (16 a cycle and
-// SM).  Measured (B200): 512 rows at 32768 tokens, 8 KV heads, 32 heads, d = 128: 359 us for
-// 273 GFLOP, 760 TFLOP/s, 47% of a library bf16 product; 5400 cycles a tile, tensor pipe
-// active 36%.  What bounds it is a stream's own chain: S to P 2800 cycles (four times a load
-// from TMEM, 32 exponentials a thread and a store), P to the next S 2600 (two groups of
-// eight products and three barriers).  Leaving out half of the products (in a copy) saved
-// 6%, and three quarters of the softmax and of the conversion 25%.  Tried and slower: a
-// second issuing thread (429 us), 16 scores at a time (542), polling instead of suspended
-// waits (684), tiles asked into L2 ahead (+10%), 64 scores kept in registers over the maximum
-// (408, registers shared out by role), everything unrolled (instruction cache).
+// SM).  Measured (B200): 512 rows at 32768 tokens, 8 KV heads, 32 heads, d = 128: 350 us for
+// 273 GFLOP, 780 TFLOP/s, 48% of a library bf16 product; 5400 cycles a tile, tensor pipe
+// active 36%.  What bounds it is a stream's own chain: S to P about 2700 cycles (loads from
+// TMEM, 128 exponentials a thread, stores), P to the next S 2600 (two groups of eight products
+// and three barriers).  Leaving out half of the products (in a copy) saved 6%, and three
+// quarters of the softmax and of the conversion 25%.  Tried and slower: a second issuing
+// thread (429 us), 16 scores at a time (542), polling instead of suspended waits (684), tiles
+// asked into L2 ahead (+10%), registers shared out by role so that 64 scores stay over the
+// maximum (408), everything unrolled (instruction cache).
 //
 // All tiles of all units (sequence, KV head, block of rows) form one list, cut evenly over
 // the CTAs.  Tiles behind a block's last position are left out where slots are positions
