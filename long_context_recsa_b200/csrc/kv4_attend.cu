@@ -29,7 +29,7 @@
 // part, 22 bits; the low part of P' is scaled by 2^11, so that it keeps its bits where P'
 // itself is below fp16's normal range).  The softmax maximum, its sum and all accumulators are fp32.
 //
-// Work.  A unit is (sequence, KV head, block of 8 to 32 rows); its cache is cut into tiles
+// Work.  A unit is (sequence, KV head, block of 8 rows; fp32: 4, 8 or 16); its cache is cut into tiles
 // of 32 tokens.  All tiles of all units form one list, cut evenly over a persistent grid
 // (so ragged batches balance); a CTA's warps take its tiles in turn, each with its own ring
 // of TMA stages, running maximum and accumulators, and meet only at the end of a unit.  A
@@ -1175,7 +1175,7 @@ cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch&
 }  // namespace
 
 int kv4_attend_counters() { return 3 * kGridMax; }
-size_t kv4_attend_part_floats(int D) { return (size_t)2 * kGridMax * 32 * (D + 2); }
+size_t kv4_attend_part_floats(int D) { return (size_t)2 * kGridMax * 16 * (D + 2); }
 
 #define KV4_ATTEND(FN, ...)                                             \
     do {                                                                \
