@@ -55,7 +55,7 @@ struct Kv4Source {
 struct Kv4Scratch {
     float* part;             // [2 * grid][rows a block][D + 2] split-softmax partials (both kernels')
     uint32_t* ucnt;          // [3 * grid] arrivals at the joins of split units (left at 0)
-    float* lse;              // [U][rows] log2 of each row's softmax sum
+    float2* stat;            // [U][rows] a row's reference m (log2 units) and 1 / sum of 2^(score - m)
 };
 
 // Rows of one attention wave: rows i0 .. i0 + w - 1 of every sequence's n rows.
@@ -87,9 +87,15 @@ size_t kv4_chunk_part_floats(int D, int rows);          // the same for kv4_laun
 cudaError_t kv4_prepare_chunk(int D);
 // bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows
 cudaError_t kv4_launch_chunk(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s);
-// renorm: after kv4_launch_chunk, whose row sums are good to 2e-6, not to fp32
+// form_stat: after kv4_launch_chunk, which leaves no Kv4Scratch::stat (its scores come from
+// keys rounded to fp16)
 cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                               const Kv4Maps& maps, int chunk, int renorm, int dtype, cudaStream_t s);
+                               const Kv4Maps& maps, int chunk, int form_stat, int dtype, cudaStream_t s);
+
+// A row's entry of Kv4Scratch::stat from its reference and sum (a row that sees no token: 0).
+__device__ __forceinline__ float2 kv4_stat(float m, float l) {
+    return l > 0.0f || l != l ? make_float2(m, 1.0f / l) : make_float2(0.0f, 0.0f);
+}
 
 // A launch that may start while the previous kernel of the stream finishes (every
 // kernel of the cache passes pdl_wait() in all its threads before it touches memory).

@@ -571,8 +571,9 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                 for (int cs = 0; cs < NCS; ++cs)
 #pragma unroll
                     for (int e = 0; e < RL; ++e) {
-                        sc[cs][2 * e] *= rsc[cs][e];
-                        sc[cs][2 * e + 1] *= rsc[cs][e];
+                        // (rounded on its own: the weights' kernel forms the same bits)
+                        sc[cs][2 * e] = __fmul_rn(sc[cs][2 * e], rsc[cs][e]);
+                        sc[cs][2 * e + 1] = __fmul_rn(sc[cs][2 * e + 1], rsc[cs][e]);
                         if (CHUNK || tail) {
                             const int lm = CHUNK ? lim[cs][e] : 0x7ffffffe;
                             if (pos0 > lm) sc[cs][2 * e] = -INFINITY;
@@ -749,9 +750,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                                        __floats2bfloat162_rn(v.z * inv, v.w * inv)};
                 *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(y);
             }
-            if (d4 == 0 && sc_.lse)
-                sc_.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] =
-                    ls > 0.0f || ls != ls ? mx + log2f(ls) : INFINITY;
+            if (d4 == 0) sc_.stat[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] = kv4_stat(mx, ls);
         };
         auto slot = [&](int64_t cta) { return 2 * cta + (cta == cta0 ? 1 : 0); };
         auto part_of = [&](int64_t cta) { return sc_.part + (size_t)slot(cta) * RB * (D + 2); };
@@ -862,14 +861,17 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 }
 
 // Accumulated weights: w[slot] += sum over the newest acc_rows rows of every sequence
-// (all G heads) of exp2(score - lse), with the scores formed again from the keys as above
-// and the rows' lse from the attention launch before it.  The rows that count are held in
-// shared memory, as many as fit a launch; a tile's codes are read once for all of them.
-// Every slot belongs to one warp (or one CTA), so sums have one order.
+// (all G heads) of 2^(score - m) / l, with the scores formed again from the keys as above (the
+// same bits) and the rows' m and l from the attention launch before it.  The difference comes
+// first, so that neither large scores nor the logarithm of l cost bits.  The rows that count
+// are held in shared memory, as many as fit a launch; a tile's codes are read once for all of
+// them.  Every slot belongs to one warp (or one CTA), so sums have one order.
 //
-// After the chunk kernel the lse come from keys rounded to fp16, which would leave 2e-6 in the
-// weights.  There a launch with SUMS goes first: it adds exp2(score - lse) by rows, which
-// gives 1 but for that error, and the second launch takes its logarithm off (`renorm`).
+// The chunk kernel's own m and l come from keys rounded to fp16; with them a row's weights
+// would not add up to 1 (2e-6 off for scores of about 10, a factor for scores of thousands).
+// There a launch with SUMS goes first, which forms m and l from these scores.  Units that lie
+// whole in a CTA leave them in stat, units that are cut leave a part a CTA: at most one such
+// unit begins in a CTA (its last) and one has begun before it, which is two slots a CTA.
 //
 // Measured: 32 us for one row of 131072 tokens x 8 KV heads (84 MB of keys, 8 of weights);
 // 128 rows a KV head of 16384 x 8: 88 us a launch, bound by the latency of scores and
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 template <int D, int T, bool CHUNK, bool SUMS>
 __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
     Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,
-    int n_blocks, int renorm) {
+    int n_blocks, int formed) {
     constexpr int NG = D / kKv4Group, RB = 8 / T, RL = 2 / T;
     using St = Stage<D>;
     using RowsT = Rows<D, T, 1>;
@@ -886,8 +888,8 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* ring = smem;
     RowsT* rs = reinterpret_cast<RowsT*>(smem + kAttendWarps * kStagesKv4 * St::kBytes);
-    float* lse = reinterpret_cast<float*>(rs + n_blocks);   // [n_blocks][RB]
-    float* row_sums = lse + n_blocks * RB;                  // SUMS: [warp][n_blocks][RB]
+    // the rows' m and 1 / l [n_blocks][RB]; SUMS: each warp's m and l [warp][n_blocks][RB]
+    float2* stat = reinterpret_cast<float2*>(rs + n_blocks);
     __shared__ Plan pl;
     __shared__ uint64_t bars[kAttendWarps][kStagesKv4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -940,6 +942,11 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
             bulk_g2s(st + St::kKp, c.kp + (u * c.R + r) * NG, St::kPars, bar);
             if (CHUNK) bulk_g2s(st + St::kPos, c.pos + u * c.R + r, kTile * 4, bar);
         };
+        const int64_t unit0 = at - tile0;              // first tile of the unit in the list
+        const int64_t cta0 = unit0 / quota, cta1 = (unit0 + tiles - 1) / quota;
+        auto cut_stat = [&](int64_t cta) {
+            return reinterpret_cast<float2*>(sc_.part) + (2 * cta + (cta == cta0 ? 1 : 0)) * n_blocks * RB;
+        };
         int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - base + step - 1) / step : 0;
         if (lane == 0 && alive)
             for (int s = 0; s < kStagesKv4 && s < mine; ++s) fetch(tile0 + base + s * step, s);
@@ -947,23 +954,29 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         if (row0 < row_end) {
             stage_rows<D, T, 1>(rs, n_blocks, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp,
                                 kAttendWarps, lane);
-            const int64_t unit0 = at - tile0;
-            const int64_t cta0 = unit0 / quota, cta1 = (unit0 + tiles - 1) / quota;
-            for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads) {
-                float x = row0 + i < row_end
-                    ? sc_.lse[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G] : INFINITY;
-                if (!SUMS && renorm && row0 + i < row_end) {
-                    float sum = 0.0f;
-#pragma unroll 4
-                    for (int64_t k = cta0; k <= cta1; ++k)
-                        sum += __ldcg(sc_.part + (2 * k + (k == cta0 ? 1 : 0)) * n_blocks * RB + i);
-                    if (sum != 0.0f) x += log2f(sum);
-                }
-                lse[i] = x;
-            }
-            if (SUMS)
+            if constexpr (SUMS) {
                 for (int i = threadIdx.x; i < kAttendWarps * n_blocks * RB; i += kAttendThreads)
-                    row_sums[i] = 0.0f;
+                    stat[i] = make_float2(kKv4MinLog2, 0.0f);
+            } else {
+                for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads) {
+                    float2 x = make_float2(0.0f, 0.0f);
+                    if (row0 + i < row_end && !(formed && cta0 != cta1)) {
+                        x = sc_.stat[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G];
+                    } else if (row0 + i < row_end) {
+                        // (in the order of the CTAs, with a running maximum)
+                        float m = kKv4MinLog2, l = 0.0f;
+#pragma unroll 4
+                        for (int64_t k = cta0; k <= cta1; ++k) {
+                            const float2 p = __ldcg(cut_stat(k) + i);
+                            const float mn = fmaxf(m, p.x);
+                            l = fmaf(p.y, ex2(p.x - mn), l * ex2(m - mn));
+                            m = mn;
+                        }
+                        x = kv4_stat(m, l);
+                    }
+                    stat[i] = x;
+                }
+            }
         }
         __syncthreads();
         for (int it = 0; it < mine; ++it) {
@@ -1002,22 +1015,37 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
                     scores16<D, T, 1>(sc, st, rs[k], qreg, qsum, rs[k].off[lane], ctr, r0, lane);
 #pragma unroll
                     for (int e = 0; e < RL; ++e) {
-                        const float f = rs[k].scale[t * RL + e], ls = lse[k * RB + t * RL + e];
+                        const float f = rs[k].scale[t * RL + e];
                         const int lm = rs[k].lim[t * RL + e];
-                        const float x0 = ex2(sc[0][2 * e] * f - ls), x1 = ex2(sc[0][2 * e + 1] * f - ls);
+                        float x0 = __fmul_rn(sc[0][2 * e], f), x1 = __fmul_rn(sc[0][2 * e + 1], f);
                         // rows that are not there have lm = -1, below every position
                         if constexpr (SUMS) {
-                            float x = (pos0 <= lm && tok < L ? x0 : 0.0f) + (pos1 <= lm && tok + 8 < L ? x1 : 0.0f);
+                            if (!(pos0 <= lm && tok < L)) x0 = -INFINITY;
+                            if (!(pos1 <= lm && tok + 8 < L)) x1 = -INFINITY;
+                            float2& ml = stat[(warp * n_blocks + k) * RB + t * RL + e];
+                            float m = ml.x, l = ml.y, x = fmaxf(x0, x1);
+                            if (__any_sync(kFull, x > m + kSlack)) {
+                                x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                                x = fmaxf(m, fmaxf(x, __shfl_xor_sync(kFull, x, 16)));
+                                l *= ex2(m - x);
+                                m = x;
+                            }
+                            x = ex2(x0 - m) + ex2(x1 - m);
                             x += __shfl_xor_sync(kFull, x, 4);
                             x += __shfl_xor_sync(kFull, x, 8);
                             x += __shfl_xor_sync(kFull, x, 16);
-                            if (g == 0) row_sums[(warp * n_blocks + k) * RB + t * RL + e] += x;
+                            if (g == 0) ml = make_float2(m, l + x);
                         } else {
+                            const float2 ml = stat[k * RB + t * RL + e];
+                            x0 = ex2(x0 - ml.x) * ml.y;
+                            x1 = ex2(x1 - ml.x) * ml.y;
                             if ((CHUNK ? pos0 : 0) <= lm) sum0 += x0;
                             if ((CHUNK ? pos1 : 0) <= lm) sum1 += x1;
                         }
                     }
                 }
+                __syncwarp();                      // (stat is read again by the whole warp)
                 if constexpr (SUMS) continue;
                 sum0 += __shfl_xor_sync(kFull, sum0, 1);
                 sum1 += __shfl_xor_sync(kFull, sum1, 1);
@@ -1055,13 +1083,20 @@ __global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
         }
         if constexpr (SUMS) {
             __syncthreads();
-            if (row0 < row_end)
-                for (int i = threadIdx.x; i < n_blocks * RB; i += kAttendThreads) {
-                    float x = 0.0f;
+            for (int i = threadIdx.x; row0 + i < row_end && i < n_blocks * RB; i += kAttendThreads) {
+                float m = kKv4MinLog2, l = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < kAttendWarps; ++k) x += row_sums[k * n_blocks * RB + i];
-                    sc_.part[(2 * (int64_t)blockIdx.x + (tile0 == 0 ? 1 : 0)) * n_blocks * RB + i] = x;
+                for (int k = 0; k < kAttendWarps; ++k) m = fmaxf(m, stat[k * n_blocks * RB + i].x);
+#pragma unroll
+                for (int k = 0; k < kAttendWarps; ++k) {
+                    const float2 p = stat[k * n_blocks * RB + i];
+                    l = fmaf(p.y, ex2(p.x - m), l);
                 }
+                if (cta0 == cta1)
+                    sc_.stat[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G] = kv4_stat(m, l);
+                else
+                    cut_stat(blockIdx.x)[i] = make_float2(m, l);
+            }
         }
         at += tile1 - tile0;
         __syncthreads();
@@ -1077,16 +1112,21 @@ template <int D, int T, int NCS>
 constexpr size_t attend_smem() {
     return 1024 + ring_bytes<D, NCS * 8 / T>() + sizeof(Rows<D, T, NCS>);
 }
+// A column set's rows and their statistics (bf16: each warp's, for SUMS).
+template <int D, int T>
+constexpr size_t weights_block_bytes() {
+    return sizeof(Rows<D, T, 1>) + (T == 1 ? kAttendWarps : 1) * sizeof(float2) * 8 / T;
+}
 template <int D, int T>
 constexpr size_t weights_smem(int blocks) {
     return 1024 + (size_t)kAttendWarps * kStagesKv4 * Stage<D>::kBytes +
-           (size_t)blocks * (sizeof(Rows<D, T, 1>) + (1 + kAttendWarps) * sizeof(float) * 8 / T);
+           (size_t)blocks * weights_block_bytes<D, T>();
 }
 // Column sets a weights launch holds: 64 KB of rows, so that two CTAs share an SM beside
 // their rings (four with half of it).
 template <int D, int T>
 constexpr int weight_blocks() {
-    return 65536 / (int)(sizeof(Rows<D, T, 1>) + (1 + kAttendWarps) * sizeof(float) * 8 / T);
+    return 65536 / (int)weights_block_bytes<D, T>();
 }
 
 // Column sets of a block: the fewest that hold the rows, up to four (the accumulators of
@@ -1149,9 +1189,11 @@ cudaError_t attend_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& 
 
 template <int D, int T>
 cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                         const Kv4Maps& maps, int chunk, int renorm, cudaStream_t s) {
+                         const Kv4Maps& maps, int chunk, int form_stat, cudaStream_t s) {
     const int rows = (qv.acc_rows < qv.w ? qv.acc_rows : qv.w) * c.G, per = 8 / T;
     constexpr int most = weight_blocks<D, T>();
+    // two slots of (m, l) a CTA for the units that are cut
+    static_assert(T == 2 || 2 * most * 8 * 2 <= 2 * 16 * (D + 2), "the parts do not hold them");
     for (int r = 0; r < rows; r += most * per) {
         int blocks = (rows - r + per - 1) / per;
         if (blocks > most) blocks = most;
@@ -1159,12 +1201,12 @@ cudaError_t weights_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch&
         const dim3 grid(148 * (smem <= 56 * 1024 ? 4 : smem <= 74 * 1024 ? 3 : 2));
         cudaError_t e = cudaSuccess;
         if constexpr (T == 1)
-            if (renorm)
+            if (form_stat)
                 e = kv4_launch(kv4_weights_kernel<D, T, true, true>, grid, kAttendThreads, smem, s, c, qv,
                                sc, maps, r, blocks, 0);
         if (e != cudaSuccess) return e;
         e = chunk ? kv4_launch(kv4_weights_kernel<D, T, true, false>, grid, kAttendThreads, smem, s, c, qv,
-                               sc, maps, r, blocks, renorm)
+                               sc, maps, r, blocks, form_stat)
                   : kv4_launch(kv4_weights_kernel<D, T, false, false>, grid, kAttendThreads, smem, s, c,
                                qv, sc, maps, r, blocks, 0);
         if (e != cudaSuccess) return e;
@@ -1196,10 +1238,10 @@ cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scr
 }
 
 cudaError_t kv4_launch_weights(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
-                               const Kv4Maps& maps, int chunk, int renorm, int dtype, cudaStream_t s) {
+                               const Kv4Maps& maps, int chunk, int form_stat, int dtype, cudaStream_t s) {
     NvtxRange nv("recsa kv4 weights");
     const int D_ = c.D;
-    KV4_ATTEND(weights_impl, c, qv, sc, maps, chunk, renorm, s);
+    KV4_ATTEND(weights_impl, c, qv, sc, maps, chunk, form_stat, s);
 }
 
 }  // namespace recsa

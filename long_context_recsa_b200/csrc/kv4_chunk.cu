@@ -801,10 +801,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                             po[(size_t)((k + e) / 4) * RB + rr] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (live && whole) {
-                    sc.lse[(int64_t)un.u * qv.w * c.G + row - qv.i0 * c.G] =
-                        any ? m - kUp + log2f(l) : INFINITY;
-                } else if (live) {
+                if (live && !whole) {
                     part[(size_t)RB * D + rr] = m;
                     part[(size_t)RB * D + RB + rr] = l;
                 }
@@ -1017,8 +1014,6 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View c, Kv4Query qv, K
         }
         *reinterpret_cast<uint4*>(out + ch * 8) = out8(o, inv);
     }
-    if (warp == 0)
-        sc.lse[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] = any ? m - kUp + log2f(l) : INFINITY;
 }
 
 // ---------------------------------------------------------------------------------
