@@ -509,21 +509,28 @@ class RecsaKV4:
         return lib.recsa_kv4_get_status(self.handle, self._on(stream))
 
     # --- conveniences (allocation + views only) -------------------------------
+    def _new(self, make, like, stream):
+        """The output of a call: it belongs to the call's stream, which may zero it too."""
+        if stream is None:
+            return make(like)
+        with torch.cuda.stream(stream):
+            return make(like)
+
     def decode(self, q: torch.Tensor, accumulate: bool = False, stream=None):
-        out = torch.empty_like(q)
+        out = self._new(torch.empty_like, q, stream)
         self.recsa_kv4_decode(q, out, accumulate, stream)
         return out
 
     def prefill(self, Q: torch.Tensor, counts=None, accumulate_rows: int = 0, stream=None):
         """Rows past a sequence's count are zeros."""
-        O = torch.empty_like(Q) if counts is None else torch.zeros_like(Q)
+        O = self._new(torch.empty_like if counts is None else torch.zeros_like, Q, stream)
         self.recsa_kv4_prefill_chunk(Q, O, counts, accumulate_rows, stream)
         return O
 
     def read(self, start: int, n: int, stream=None):
-        k = torch.empty(self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim,
-                        dtype=self.cfg.torch_dtype, device=self.device)
-        v = torch.empty_like(k)
+        shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
+        k, v = (self._new(lambda x: torch.empty(x, dtype=self.cfg.torch_dtype, device=self.device),
+                          shape, stream) for _ in range(2))
         self.recsa_kv4_read(start, n, k, v, stream)
         return k, v
 
