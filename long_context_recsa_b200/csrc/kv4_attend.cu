@@ -24,10 +24,19 @@
 //     fp32 beside it.
 //
 // Precision.  q enters as fp16 scaled by a power of two to [2^10, 2^11): a bf16 q is exact
-// there.  P' enters as fp16, off by at most 2^-12 relative, less than bf16's own 2^-9 of
-// the output.  fp32 tensors use two fp16 columns a row for q and for P' (high and low
-// part, 22 bits; the low part of P' is scaled by 2^11, so that it keeps its bits where P'
-// itself is below fp16's normal range).  The softmax maximum, its sum and all accumulators are fp32.
+// there but for elements below 2^-24 of the row's largest (off by 2^-32 of that).  P' enters as
+// fp16, off by at most 2^-11 relative, less than bf16's own 2^-8 of the output.  fp32 tensors
+// use two fp16 columns a row for q and for P' (high and low part, 22 bits; the low part of P'
+// is scaled by 2^11, so that it keeps its bits where P' itself is below fp16's normal range).
+// The softmax maximum, its sum and all accumulators are fp32.
+//
+// Each row and group of dims has its own scale of P' (`up`): p s may span any range, and what
+// falls below fp16 is less than 2^-30 of the row's and group's largest p s so far.  So a huge
+// value hurts no row that gives it no weight, and a heavy token of tiny value no background
+// behind it.  A P' that passes 2^14 lowers its scale and O with it; where the running maximum
+// moves, O as a sum falls, which raises the scale instead.  (One scale a unit, from the largest
+// value ever written, took 667 us instead of 689 at 4 x 524288 and 10.0 instead of 10.9 at 37
+// tokens, but lost every value below 2^-24 of that one.)
 //
 // Work.  A unit is (sequence, KV head, block of 8 rows; fp32: 4, 8 or 16); its cache is cut into tiles
 // of 32 tokens.  All tiles of all units form one list, cut evenly over a persistent grid
@@ -56,6 +65,9 @@ constexpr int kStagesKv4 = 2;
 constexpr int kGridMax = 148 * 4;
 constexpr int kJoin = 16;            // partial results that one CTA joins
 constexpr float kSlack = 6.0f;       // p may reach 2^6 before the running maximum moves
+constexpr float kMostUp = 0x1p120f;  // largest scale of P', and the first
+constexpr int kMostLog2 = 14;        // P' moves its scale where it passes 2^14 ..
+constexpr float kSetUp = 0x1p-8f;    // .. which is set so that the largest P' is 2^5 to 2^6
 constexpr float kLowUp = 2048.0f;    // fp32 tensors: scale of the low part of P' (its own column)
 
 template <int D>
@@ -163,6 +175,30 @@ __device__ __forceinline__ float pow2i(int e) {
 }
 __device__ __forceinline__ int exponent_of(float x) {   // floor(log2 |x|), -127 for 0
     return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
+}
+
+// The largest P' of a lane: fp16 pairs as integers (no P' is negative), fp32 tensors' high parts.
+template <int T>
+struct Largest {
+    uint32_t x = 0;
+    float y = 0.0f;
+    __device__ __forceinline__ void add(uint32_t a, uint32_t b) { x = __vimax3_u16x2(x, a, b); }
+    __device__ __forceinline__ void add(float a, float b) { y = fmaxf(y, fmaxf(a, b)); }
+    __device__ __forceinline__ bool over() const {
+        if (T == 2) return y > (float)(1 << kMostLog2);
+        constexpr uint32_t most = (uint32_t)(kMostLog2 + 15) << 10;   // as fp16
+        return x >= (most + 1u) << 16 || (x & 0xffffu) > most;
+    }
+};
+
+// Scales row e of a lane in the accumulators of one group's output.
+template <int T>
+__device__ __forceinline__ void scale_row(float (&o)[2][4], int e, float f) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            if (T == 2 || (z & 1) == e) o[k][z] *= f;
 }
 
 // Rows of a column set (8 MMA columns): one column a row, or a high and a low column.
@@ -488,13 +524,8 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         stage_rows<D, T, NCS>(&rs, 1, c, qv, b, h, row0, row_end, n_b, c.seen[b], warp, kAttendWarps, lane);
         __syncthreads();
 
-        // V's steps enter P' scaled so that the unit's largest is at most 2^8
-        // (s <= 2.02 vmax / 15 < 2^ev), so P' stays below 2^14
-        const int e0 = exponent_of(__uint_as_float(c.vmax[u])) - 1, ev = e0 < -118 ? -118 : e0;
-        const float vf = pow2i(8 - ev);
-        const float vinv = pow2i(ev - 8);
-
         float O[NCS][NG][2][4], bias[NCS][RL][NG], m[NCS][RL], l[NCS][RL], rsc[NCS][RL];
+        float up[NCS][RL][NG];                         // of P': O is `up` times the sum of p s code
         int lim[NCS][RL];
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
@@ -511,7 +542,10 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                 rsc[cs][e] = rs.scale[cs * RS + t * RL + e];
                 lim[cs][e] = rs.lim[cs * RS + t * RL + e];
 #pragma unroll
-                for (int j = 0; j < NG; ++j) bias[cs][e][j] = 0.0f;
+                for (int j = 0; j < NG; ++j) {
+                    bias[cs][e][j] = 0.0f;
+                    up[cs][e][j] = kMostUp;
+                }
             }
         }
         uint4 qreg[NCS == 1 ? NG : 1];
@@ -582,6 +616,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         grow |= fmaxf(sc[cs][2 * e], sc[cs][2 * e + 1]) > m[cs][e] + kSlack;
                     }
                 if (__any_sync(kFull, grow)) {
+                    const bool empty = it == 0 && half == 0;   // no sums yet
 #pragma unroll
                     for (int cs = 0; cs < NCS; ++cs)
 #pragma unroll
@@ -591,22 +626,18 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                             x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
                             const float mn = fmaxf(m[cs][e], x);
-                            const float f = ex2(m[cs][e] - mn);
+                            const float f = ex2(m[cs][e] - mn), inv = __fdividef(1.0f, f);
                             m[cs][e] = mn;
+                            if (empty) continue;
                             l[cs][e] *= f;
 #pragma unroll
                             for (int j = 0; j < NG; ++j) {
                                 bias[cs][e][j] *= f;
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    if constexpr (T == 1) {
-                                        O[cs][j][k][e] *= f;
-                                        O[cs][j][k][2 + e] *= f;
-                                    } else {
-#pragma unroll
-                                        for (int z = 0; z < 4; ++z) O[cs][j][k][z] *= f;
-                                    }
-                                }
+                                // O falls by f as a sum: its scale rises, O stays, up to a limit
+                                const float y = up[cs][e][j] * inv;
+                                if (!(y <= kMostUp))
+                                    scale_row<T>(O[cs][j], e, __fdividef(f * kMostUp, up[cs][e][j]));
+                                up[cs][e][j] = y <= kMostUp ? y : kMostUp;
                             }
                         }
                 }
@@ -618,12 +649,75 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         sc[cs][2 * e + 1] = ex2(sc[cs][2 * e + 1] - m[cs][e]);
                         l[cs][e] += sc[cs][2 * e] + sc[cs][2 * e + 1];
                     }
-                float pv[NCS][2 * RL];         // in the scale of P'
+                // P' and the offsets' share.  (Scale times p first: a step alone may pass fp32,
+                // and p = 0 must stay 0.)
+                uint32_t b0[NCS][NG], b1[NCS][NG], nan0 = 0, nan1 = 0;
+                auto form = [&] {
+                    Largest<T> most;
 #pragma unroll
-                for (int cs = 0; cs < NCS; ++cs)
+                    for (int j = 0; j < NG; ++j) {
+                        const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
 #pragma unroll
-                    for (int e = 0; e < 2 * RL; ++e) pv[cs][e] = sc[cs][e] * vf;
-                uint32_t nan0 = 0, nan1 = 0;
+                        for (int cs = 0; cs < NCS; ++cs) {
+                            const float u0 = up[cs][0][j], x0 = sc[cs][0] * u0 * s0, x1 = sc[cs][1] * u0 * s1;
+                            if constexpr (T == 1) {
+                                const float u1 = up[cs][1][j];
+                                b0[cs][j] = pack_h2(x0, sc[cs][2] * u1 * s0);
+                                b1[cs][j] = pack_h2(x1, sc[cs][3] * u1 * s1);
+                                most.add(b0[cs][j], b1[cs][j]);
+                            } else {
+                                const float h0 = __half2float(__float2half_rn(x0));
+                                const float h1 = __half2float(__float2half_rn(x1));
+                                b0[cs][j] = pack_h2(h0, (x0 - h0) * kLowUp);
+                                b1[cs][j] = pack_h2(h1, (x1 - h1) * kLowUp);
+                                most.add(h0, h1);
+                            }
+                        }
+                    }
+                    return __any_sync(kFull, most.over());
+                };
+                if (form()) {
+                    // Scales with which a P' passes the limit are set anew.  A row's largest p s
+                    // of each group over the lanes that hold its tokens: values are handed out
+                    // while they are compared, so that a lane ends with an eighth of them.
+                    constexpr int NV = NCS * RL * NG, NE = NV < 8 ? 1 : NV / 8;
+                    float y[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int cs = i / (RL * NG), e = i / NG % RL, j = i % NG;
+                        y[i] = fmaxf(sc[cs][2 * e] * kv4_step(p0[j]), sc[cs][2 * e + 1] * kv4_step(p1[j]));
+                    }
+                    int n = NV;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        const bool hi = (lane & o) != 0;
+                        if (n == 1) {
+                            y[0] = fmaxf(y[0], __shfl_xor_sync(kFull, y[0], o));
+                        } else {
+                            n /= 2;
+#pragma unroll
+                            for (int i = 0; i < NV / 2; ++i)
+                                if (i < n) {
+                                    const float r = __shfl_xor_sync(kFull, hi ? y[i] : y[i + n], o);
+                                    y[i] = fmaxf(hi ? y[i + n] : y[i], r);
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) y[i] = pow2i(kMostLog2 - 1 - exponent_of(y[i]));
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int cs = i / (RL * NG), e = i / NG % RL, j = i % NG;
+                        const int from = i * 2 / NV * 4 + i * 4 / NV % 2 * 8 + (NV < 8 ? 0 : i * 8 / NV % 2 * 16);
+                        const float most = __shfl_sync(kFull, y[i % NE], from + t);
+                        if (up[cs][e][j] > most) {
+                            const float x = most * kSetUp;
+                            scale_row<T>(O[cs][j], e, __fdividef(x, up[cs][e][j]));
+                            up[cs][e][j] = x;
+                        }
+                    }
+                    form();
+                }
 #pragma unroll
                 for (int j2 = 0; j2 < NG; j2 += 2) {
                     uint32_t w[4];
@@ -641,9 +735,8 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         const uint32_t a5 = ctr.high(wa >> 8);
                         const uint32_t a6 = ctr.low(wb >> 8);
                         const uint32_t a7 = ctr.high(wb >> 8);
-                        const float s0 = kv4_step(p0[j]), s1 = kv4_step(p1[j]);
-                        float c0 = fmaf(8.0f, s0, kv4_off(p0[j]));
-                        float c1 = fmaf(8.0f, s1, kv4_off(p1[j]));
+                        float c0 = fmaf(8.0f, kv4_step(p0[j]), kv4_off(p0[j]));
+                        float c1 = fmaf(8.0f, kv4_step(p1[j]), kv4_off(p1[j]));
                         if (CHUNK) {
                             // a NaN group must not reach rows that do not see its token
                             if (c0 != c0) { c0 = 0.0f; nan0 |= 1u << j; }
@@ -651,23 +744,13 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         }
 #pragma unroll
                         for (int cs = 0; cs < NCS; ++cs) {
-                            uint32_t b0, b1;
-                            if constexpr (T == 1) {
-                                b0 = movm(pack_h2(pv[cs][0] * s0, pv[cs][2] * s0));
-                                b1 = movm(pack_h2(pv[cs][1] * s1, pv[cs][3] * s1));
-                            } else {
-                                const float x0 = pv[cs][0] * s0, x1 = pv[cs][1] * s1;
-                                const float h0 = __half2float(__float2half_rn(x0));
-                                const float h1 = __half2float(__float2half_rn(x1));
-                                b0 = movm(pack_h2(h0, (x0 - h0) * kLowUp));
-                                b1 = movm(pack_h2(h1, (x1 - h1) * kLowUp));
-                            }
 #pragma unroll
                             for (int e = 0; e < RL; ++e)
                                 bias[cs][e][j] = fmaf(sc[cs][2 * e], c0,
                                                       fmaf(sc[cs][2 * e + 1], c1, bias[cs][e][j]));
-                            mma16816(O[cs][j][0], a0, a1, a2, a3, b0, b1);
-                            mma16816(O[cs][j][1], a4, a5, a6, a7, b0, b1);
+                            const uint32_t x0 = movm(b0[cs][j]), x1 = movm(b1[cs][j]);
+                            mma16816(O[cs][j][0], a0, a1, a2, a3, x0, x1);
+                            mma16816(O[cs][j][1], a4, a5, a6, a7, x0, x1);
                         }
                     }
                 }
@@ -725,10 +808,11 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         v.z = fmaf(O[cs][j][1][1], 1.0f / kLowUp, O[cs][j][1][0]);
                         v.w = fmaf(O[cs][j][1][3], 1.0f / kLowUp, O[cs][j][1][2]);
                     }
-                    v.x = fmaf(v.x, vinv, bs);
-                    v.y = fmaf(v.y, vinv, bs);
-                    v.z = fmaf(v.z, vinv, bs);
-                    v.w = fmaf(v.w, vinv, bs);
+                    const float down = __fdividef(1.0f, up[cs][e][j]);
+                    v.x = fmaf(v.x, down, bs);
+                    v.y = fmaf(v.y, down, bs);
+                    v.z = fmaf(v.z, down, bs);
+                    v.w = fmaf(v.w, down, bs);
                     *reinterpret_cast<float4*>(red + ((size_t)warp * RB + r) * D + j * 32 + g * 4) = v;
                 }
             }
@@ -873,11 +957,13 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 // whole in a CTA leave them in stat, units that are cut leave a part a CTA: at most one such
 // unit begins in a CTA (its last) and one has begun before it, which is two slots a CTA.
 //
+// Registers: fp32 rows take 168 (three CTAs an SM); held to 128, 16 x 3999 took 3 us more.
+//
 // Measured: 32 us for one row of 131072 tokens x 8 KV heads (84 MB of keys, 8 of weights);
 // 128 rows a KV head of 16384 x 8: 88 us a launch, bound by the latency of scores and
 // exponentials at eight warps an SM.
 template <int D, int T, bool CHUNK, bool SUMS>
-__global__ void __launch_bounds__(kAttendThreads) kv4_weights_kernel(
+__global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_kernel(
     Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,
     int n_blocks, int formed) {
     constexpr int NG = D / kKv4Group, RB = 8 / T, RL = 2 / T;

@@ -1,0 +1,155 @@
+"""Attention over the 4-bit KV cache where keys and values span many magnitudes: a huge token
+that no row gives weight to, that a row does not see, or that was evicted; groups of dims of
+unequal size; a heavy token of tiny value before a long faint background.
+
+Tolerances, from the arithmetic, of one output dim of one row with probabilities p_t:
+  * probabilities: off by twice a score's error (relative), 16 * 2^-24 * S with S = 2 * scale *
+    sum |q| |K_t| over the tokens that have weight, plus 2^-20 for exp2 and the sums: times
+    sum p |V|.
+  * P' (probability times step, 2^-11; fp32 tensors 2^-21) meets codes of at most 8 in
+    magnitude: times 8 sum p s.  Below fp16's normal numbers it is off by 2^-25 where the
+    largest of the row and group is at least 2^8: N tokens add at most N * 2^-33 of the
+    largest p s, times 8 (fp32 tensors: the low part is scaled by 2^11, 2^-44).
+  * on the tensor cores K and V enter as fp16 (2^-11; S then adds 2^-12 * S) and P too.
+  * the output is rounded to its type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as O
+from tests import test_gpu_kv4 as T
+
+pytestmark = pytest.mark.gpu
+R = T.R                                                  # the fixture
+
+
+def floor_of(u, s, q, at, dtype, tc):
+    """Tolerance [d] of one row q [d] at position `at`, beside the output's own rounding."""
+    p = u.probabilities(q, at)
+    heavy = p > 2.0 ** -60
+    S = 2 * u.scale * (np.abs(u.k[heavy]) @ np.abs(q)).max()
+    delta = 16 * 2.0 ** -24 * S + (2.0 ** -12 * S if tc else 0)
+    pv = p[heavy] @ np.abs(u.v[heavy])
+    steps = (p[:, None] * s).repeat(32, 1)
+    floor = (2 * delta + 2.0 ** -20) * pv + T.PROB[dtype] * 8 * steps.sum(0)
+    floor += 8 * len(p) * 2.0 ** (-33 if dtype == "bf16" else -44) * steps.max(0)
+    return floor + (2 * 2.0 ** -11 * pv if tc else 0)
+
+
+def run(R, dtype, d, k, v, Q, n, lengths=None, prepare=None):
+    """One KV head: k, v [L][d], Q [n][G][d]; n = 0: a decode of Q[0].  Compares all rows."""
+    L, G = len(k), Q.shape[1]
+    k, v, Q = (x.to(T.DT[dtype]) for x in (k, v, Q))
+    cfg = R.Config(head_dim=d, n_q_heads=G, n_kv_heads=1, dtype=dtype)
+    kv4 = R.RecsaKV4(cfg, L, 1, max_queries=max(n, 1))
+    kv4.recsa_kv4_build(k.cuda()[None, None], v.cuda()[None, None], [L])
+    u = O.Unit(d)
+    u.append(T.np64(k), T.np64(v))
+    s = O.quantize(T.np64(v))[1]
+    if prepare:
+        s = prepare(kv4, u, s)
+    if n == 0:
+        out = kv4.decode(Q[:1].cuda().contiguous())[0][None]
+    else:
+        out = kv4.prefill(Q[None].cuda())[0]
+    tc = T.on_tensor_cores(dtype, n * G)
+    out = T.np64(out)
+    for i in range(max(n, 1)):
+        at = u.seen - max(n, 1) + i
+        for g in range(G):
+            q = T.np64(Q[i, g])
+            want = u.attend(q[None], at)[0]
+            tol = T.HALF[dtype] * np.abs(want) * 1.01 + floor_of(u, s, q, at, dtype, tc) + 1e-40
+            err = np.abs(out[i, g] - want)
+            assert (err <= tol).all(), (i, g, (err / tol).max(), out[i, g][err > tol][:4], want[err > tol][:4])
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+def normal(L, d, n, G, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(L, d, generator=g), torch.randn(L, d, generator=g),
+            torch.randn(max(n, 1), G, d, generator=g))
+
+
+# (dtype, d, n, G): decode, chunks of few rows, chunks of fp32
+FORMS = [("bf16", 128, 0, 4), ("bf16", 64, 0, 8), ("f32", 64, 0, 2), ("f32", 128, 0, 8), ("bf16", 128, 4, 2),
+         ("bf16", 64, 8, 1), ("f32", 128, 5, 1), ("f32", 64, 30, 4)]
+
+
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("dtype,d,n,G", FORMS)
+def test_a_huge_value_without_weight(R, dtype, d, n, G, big):
+    """Its key points away from every query: p = exp(-60 or less)."""
+    k, v, Q = normal(300, d, n, G, 1)
+    Q[..., 0] = 6.0
+    k[:, 0] = 0
+    k[17, 0] = -40.0 * d ** 0.5
+    v[17] *= big
+    run(R, dtype, d, k, v, Q, n)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 40])
+@pytest.mark.parametrize("dtype,d,n,G", [f for f in FORMS if f[2]])
+def test_a_huge_token_that_some_rows_do_not_see(R, dtype, d, n, G, big):
+    L = 200
+    k, v, Q = normal(L, d, n, G, 2)
+    v[L - 2] *= big
+    run(R, dtype, d, k, v, Q, n)
+
+
+@pytest.mark.parametrize("dtype,d,n,G", FORMS)
+def test_a_huge_token_that_was_evicted(R, dtype, d, n, G):
+    L = 260
+    k, v, Q = normal(L, d, n, G, 3)
+    k[100] *= 2.0 ** 40
+    v[100] *= 2.0 ** 40
+
+    def evict(kv4, u, s):
+        u.w = np.ones(L)
+        u.w[[100, 7]] = 0.0
+        kv4.weights()[0, 0, :L] = torch.from_numpy(u.w).float().cuda()
+        kv4.recsa_kv4_evict(L - 2, 0, 20)
+        before = u.pos.copy()
+        u.evict(L - 2, 0, 20)
+        return s[[list(before).index(p) for p in u.pos]]
+
+    run(R, dtype, d, k, v, Q, n, prepare=evict)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("dtype,d,n,G", FORMS)
+def test_groups_of_unequal_size(R, dtype, d, n, G, big):
+    """The dims of one group are larger than the others', in all tokens: every group's outputs
+    are right by their own size."""
+    k, v, Q = normal(300, d, n, G, 4)
+    v[:, 32:64] *= big
+    run(R, dtype, d, k, v, Q, n)
+
+
+@pytest.mark.parametrize("tiny", [2.0 ** -20, 2.0 ** -60])
+@pytest.mark.parametrize("dtype,d,n,G", FORMS)
+def test_a_few_tokens_are_smaller(R, dtype, d, n, G, tiny):
+    """Rows whose weight lies on tokens of tiny value, among others that have none."""
+    k, v, Q = normal(300, d, n, G, 5)
+    Q[..., 0] = 6.0
+    k[:, 0] = -40.0 * d ** 0.5
+    k[40:45, 0] = 0
+    v[40:45] *= tiny
+    run(R, dtype, d, k, v, Q, n)
+
+
+@pytest.mark.parametrize("dtype,d,n,G", [f for f in FORMS if f[2] < 10])
+def test_a_heavy_token_of_tiny_value_before_a_faint_background(R, dtype, d, n, G):
+    """One token takes nearly all weight and has almost no value; 40000 others share 2^-5 of it
+    and make the output; one value is 2^12 times the others' and has no weight."""
+    L = 40000
+    k, v, Q = normal(L, d, n, G, 6)
+    k *= 0.02
+    Q[..., 0] = 8.0
+    k[:, 0] = -20.0 * 0.6931 * d ** 0.5 / 8
+    k[0, 0] = 0.0
+    k[9, 0] = -60.0 * d ** 0.5
+    v[0] *= 2.0 ** -20
+    v[1:] += 0.5
+    v[9] *= 2.0 ** 12
+    run(R, dtype, d, k, v, Q, n)
