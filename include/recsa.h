@@ -413,7 +413,10 @@ RECSA_API recsa_status recsa_kv4_decode(recsa_kv4* kv4, const void* q, void* out
  * the cached tokens up to that position.  Rows i >= n_b are neither read nor written.  A
  * count out of range, or above P_b, is recorded as RECSA_E_DEVICE and its rows are skipped.
  * A row that sees no token gets zeros.  accumulate_rows: the newest that many rows of each
- * sequence add to the weights as recsa_kv4_decode does (0: none). */
+ * sequence add to the weights as recsa_kv4_decode does (0: none).
+ * Keys and values may span any magnitudes.  A bf16 chunk of more than 8 rows a KV head takes a
+ * far slower form for a sequence in which one group's largest |value| since the last build is
+ * more than 2^24 times another's (groups of zeros aside). */
 RECSA_API recsa_status recsa_kv4_prefill_chunk(recsa_kv4* kv4, const void* Q, int32_t n,
                                                const int32_t* counts, void* O,
                                                int32_t accumulate_rows, void* stream);

@@ -30,8 +30,11 @@ struct Kv4View {
     float* w;                // [U][R]; 0 past the length
     int64_t* len;            // [B] rows in use
     int64_t* seen;           // [B] tokens appended so far: the next token's position
-    uint32_t* kmax;          // [U] bits of the largest |value| ever written (a bound)
+    uint32_t* kmax;          // [U] bits of the largest |value| written since the last build (a bound)
     uint32_t* vmax;
+    uint32_t* kmin;          // [U] bits of the smallest group's largest |value| (but groups of 0)
+    uint32_t* vmin;
+    uint32_t* wide;          // [B] 1 where a unit's minimum lies 2^24 below its maximum: kv4_is_wide
     uint32_t* status;
     uint32_t* done;          // CTA arrival counter of append and evict (left at 0)
     int B, Hkv, Hq, G, D;
@@ -85,7 +88,8 @@ cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scr
                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s);
 size_t kv4_chunk_part_floats(int D, int rows);          // the same for kv4_launch_chunk
 cudaError_t kv4_prepare_chunk(int D);
-// bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows
+// bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows, of keys and
+// values as fp16; in fp32 for sequences whose magnitudes span more than that holds (wide)
 cudaError_t kv4_launch_chunk(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc, cudaStream_t s);
 // form_stat: after kv4_launch_chunk, which leaves no Kv4Scratch::stat (its scores come from
 // keys rounded to fp16)
@@ -118,6 +122,11 @@ inline cudaError_t kv4_launch(void (*kern)(P...), dim3 grid, int threads, size_t
 // ---------------------------------------------------------------------------------
 __device__ __forceinline__ float kv4_step(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float kv4_off(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Groups of keys or values from `least` to `most` in size: more than fp16 holds, scaled by `most`
+// to 2^13?  (2^-24 of it is 2^-11 there, off by 2^-14 of itself; below, bits are lost.)
+constexpr float kKv4Wide = 0x1p-24f;
+__device__ __forceinline__ bool kv4_is_wide(float least, float most) { return least < most * kKv4Wide; }
 
 // Rows of sequence b in a call of n rows (a count outside 0..n is recorded and taken as 0).
 __device__ __forceinline__ int64_t kv4_count(const int32_t* counts, int b, int64_t n, uint32_t* st) {

@@ -17,7 +17,7 @@ struct Kv4Layout {
     int D, G, esize;
     int64_t R, U;
     size_t o_kc, o_vc, o_kp, o_vp, o_pos, o_w, cache_bytes;
-    size_t o_status, o_done, o_len, o_seen, o_kmax, o_vmax, o_ucnt, o_stat, o_part, o_lists, ws_bytes;
+    size_t o_status, o_done, o_len, o_seen, o_kmax, o_vmax, o_kmin, o_vmin, o_wide, o_ucnt, o_stat, o_part, o_lists, ws_bytes;
 };
 
 // Rows (chunk rows times heads of a group) of one wave and KV head that kv4_launch_chunk takes:
@@ -59,6 +59,9 @@ recsa_status kv4_layout(const recsa_config* c, int64_t cap, int B, int Qmax, Kv4
     L->o_seen = w;   w = up256(w + sizeof(int64_t) * B);
     L->o_kmax = w;   w = up256(w + sizeof(uint32_t) * L->U);
     L->o_vmax = w;   w = up256(w + sizeof(uint32_t) * L->U);
+    L->o_kmin = w;   w = up256(w + sizeof(uint32_t) * L->U);
+    L->o_vmin = w;   w = up256(w + sizeof(uint32_t) * L->U);
+    L->o_wide = w;   w = up256(w + sizeof(uint32_t) * B);
     L->o_ucnt = w;   w = up256(w + sizeof(uint32_t) * kv4_attend_counters());
     L->o_stat = w;   w = up256(w + sizeof(float2) * (size_t)Qmax * c->n_q_heads);
     size_t part = kv4_attend_part_floats(L->D);
@@ -200,6 +203,9 @@ recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t b
     c.seen = (int64_t*)(ws + L.o_seen);
     c.kmax = (uint32_t*)(ws + L.o_kmax);
     c.vmax = (uint32_t*)(ws + L.o_vmax);
+    c.kmin = (uint32_t*)(ws + L.o_kmin);
+    c.vmin = (uint32_t*)(ws + L.o_vmin);
+    c.wide = (uint32_t*)(ws + L.o_wide);
     c.B = batch;
     c.Hkv = cfg->n_kv_heads;
     c.Hq = cfg->n_q_heads;

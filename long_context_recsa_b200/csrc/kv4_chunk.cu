@@ -13,8 +13,10 @@
 //
 // Eight warps turn the codes into fp16: (w & 0x000f000f) | 0x64006400 is 1024 + code in both
 // halves, less 1024 is the code, and one HFMA2 gives lo + s * code, rounded once (2^-11 of
-// the value).  K, V and q are scaled by powers of two into fp16's range (the largest |K|
-// and |V| of a unit are kept by the writes); a bf16 q is exact there.  P is scaled to at most
+// the value).  K, V and q are scaled by powers of two into fp16's range: the writes keep the
+// largest and the smallest size of a unit's groups, and a sequence in which they are 2^24 apart
+// is left to wide_rows(), since below that groups would lose bits.  A bf16 q is exact but for
+// elements below 2^-26 of the row's largest (off by 2^-35 of that).  P is scaled to at most
 // 2^14: its rounding is 2^-11 relative down to 2^-28 of the largest.  The running reference
 // (a score of the row) moves only when a score passes it by 6 (in log2), so O is seldom
 // rescaled; it, the sum of P, S and O are fp32.
@@ -80,6 +82,7 @@ struct ChunkPlan {
     int64_t first[RECSA_MAX_BATCH];       // tokens that the first block's rows see, + 127; -1: all
     int tmax[RECSA_MAX_BATCH];            // tiles of the whole cache
     int nrb[RECSA_MAX_BATCH];
+    int wide_rows[RECSA_MAX_BATCH];       // rows of a wide sequence (it has no block here), else 0
     int lg_step;                          // log2 of the positions a block adds
 };
 
@@ -121,6 +124,7 @@ __device__ __forceinline__ void make_chunk_plan(ChunkPlan& pl, const Kv4View& c,
         v[k] = 0;
         if (b < c.B) {
             const int64_t L = c.len[b], seen = c.seen[b];
+            const bool wide = c.wide[b] != 0;
             int n_b = (int)kv4_count(qv.counts, b, qv.n, c.status);
             if (n_b > seen) {             // more rows than tokens: none has a position
                 set_status(c.status, kStatusBadQuery);
@@ -128,7 +132,8 @@ __device__ __forceinline__ void make_chunk_plan(ChunkPlan& pl, const Kv4View& c,
             }
             int rows = n_b - qv.i0;
             rows = rows < 0 ? 0 : rows < qv.w ? rows : qv.w;
-            pl.nrb[b] = (rows * c.G + RB - 1) / RB;
+            pl.nrb[b] = wide ? 0 : (rows * c.G + RB - 1) / RB;
+            pl.wide_rows[b] = wide ? rows * c.G : 0;
             pl.tmax[b] = (int)((L + kTok - 1) / kTok);
             pl.first[b] = L == seen ? seen - n_b + qv.i0 + ((int64_t)RB >> lg_g) + 127 : -1;
             v[k] = c.Hkv * tiles_before(pl, b, pl.nrb[b]);
@@ -960,12 +965,96 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     }
 }
 
+// 32 rows of a unit of a wide sequence (kv4_is_wide), in plain fp32: a lane a row.  Tiles of 16
+// tokens: a warp forms the scores of two, then every warp the probabilities (the same ones) and
+// its eighth of the output's dims; tokens that a row does not see are left out there, as a NaN
+// must not reach it.  Such data is not expected, so this is short rather than fast, and stands in
+// the join's launch: a launch of the other attention kernel cost every call 4 to 6 us.
+constexpr int kWideTok = 16;
+template <int D>
+struct WideSmem {
+    float q[32][D + 1], x[kWideTok][D], s[kWideTok][32];
+    int32_t pos[kWideTok];
+};
+template <int D>
+__device__ __noinline__ void wide_rows(WideSmem<D>& sm, const Kv4View& c, const Kv4Query& qv, int u,
+                                       int rel, int rows) {
+    constexpr int E = D / 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = u / c.Hkv, h = u % c.Hkv;
+    const int n_b = qv.counts ? qv.counts[b] : qv.n;
+    const int row = qv.i0 * c.G + rel + lane, row_end = qv.i0 * c.G + rows;
+    const int i = row / c.G, g = row % c.G;
+    const int64_t L = c.len[b], at = (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D;
+    const int lim = row < row_end ? (int)(c.seen[b] - n_b + i) : -1;
+    for (int d = warp; d < D; d += 8)
+        sm.q[lane][d] = row < row_end ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(qv.q)[at + d])
+                                      : 0.0f;
+    auto load = [&](const uint8_t* codes, const uint32_t* pars, int64_t t0) {
+        for (int k = threadIdx.x; k < kWideTok * (D / 8); k += 256) {
+            const int r = k / (D / 8), w = k % (D / 8);
+            const int64_t slot = u * c.R + t0 + r;   // (R is a multiple of whole tiles)
+            const uint32_t code = reinterpret_cast<const uint32_t*>(codes)[slot * (D / 8) + w];
+            const uint32_t par = pars[slot * (D / 32) + w / 4];
+#pragma unroll 2
+            for (int e = 0; e < 8; ++e)
+                sm.x[r][w * 8 + e] = fmaf(kv4_step(par), (float)((code >> (4 * e)) & 15u), kv4_off(par));
+        }
+    };
+    const float scale = c.scale * 1.4426950408889634f;
+    float o[E], m = kKv4MinLog2, l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 1
+    for (int64_t t0 = 0; t0 < L; t0 += kWideTok) {
+        __syncthreads();
+        load(c.kc, c.kp, t0);
+        if (threadIdx.x < kWideTok)
+            sm.pos[threadIdx.x] = t0 + threadIdx.x < L ? c.pos[u * c.R + t0 + threadIdx.x] : 0x7fffffff;
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < kWideTok / 8; ++k) {
+            float s = 0.0f;
+#pragma unroll 8
+            for (int d = 0; d < D; ++d) s = fmaf(sm.q[lane][d], sm.x[warp * (kWideTok / 8) + k][d], s);
+            sm.s[warp * (kWideTok / 8) + k][lane] = s * scale;
+        }
+        __syncthreads();
+        load(c.vc, c.vp, t0);
+        __syncthreads();
+        float mn = m;
+#pragma unroll 4
+        for (int k = 0; k < kWideTok; ++k)
+            if (sm.pos[k] <= lim) mn = fmaxf(mn, sm.s[k][lane]);
+        const float f = ex2(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll 1
+        for (int k = 0; k < kWideTok; ++k) {
+            if (sm.pos[k] > lim) continue;
+            const float p = ex2(sm.s[k][lane] - m);
+            l += p;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(p, sm.x[k][warp * E + e], o[e]);
+        }
+    }
+    if (row >= row_end) return;
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(qv.out) + at + warp * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<__nv_bfloat162*>(out + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+}
+
 // Joins the parts of the units that were cut.  Grid: x = 32 rows, y = unit; a lane a row, a
 // warp some of the 8-dim pieces.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View c, Kv4Query qv, Kv4Scratch sc, int RB,
-                                                       int ctas) {
+__global__ void __launch_bounds__(256, 3) kv4_join_kernel(const __grid_constant__ Kv4View c,
+                                                          const __grid_constant__ Kv4Query qv,
+                                                          Kv4Scratch sc, int RB, int ctas) {
     __shared__ ChunkPlan pl;
+    __shared__ WideSmem<D> wide;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
@@ -973,6 +1062,10 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4View c, Kv4Query qv, K
     __syncthreads();
     const int u = blockIdx.y, b = u / c.Hkv, h = u % c.Hkv;
     const int rel = blockIdx.x * 32, rb = rel / RB, rr = rel % RB + lane;
+    if (rel < pl.wide_rows[b]) {
+        wide_rows<D>(wide, c, qv, u, rel, pl.wide_rows[b]);
+        return;
+    }
     if (rb >= pl.nrb[b]) return;
     const int64_t quota = chunk_quota(pl.pre[c.B], ctas);
     const int64_t start = pl.pre[b] + h * tiles_before(pl, b, pl.nrb[b]) + tiles_before(pl, b, rb);

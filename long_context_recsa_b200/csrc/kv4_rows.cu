@@ -20,6 +20,7 @@ constexpr int kThreadsRows = 256;
 constexpr int kUnroll = 2;           // rows of a lane that are loaded before the first is used
 constexpr int kTilesRows = 8;        // rows of a lane in all, at most
 constexpr int kReadRows = 4;         // rows of a lane in the read back
+constexpr uint32_t kInfBits = 0x7f800000u;
 
 // 16 dims of a row as they are stored: two 16-byte words of bf16, four of fp32.
 template <typename T> struct Raw { uint4 a[(int)sizeof(T)]; };
@@ -206,10 +207,11 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_clear_kernel(Kv4View c) {
         reinterpret_cast<float4*>(c.w)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (i0 < c.B * c.Hkv) {
-        c.kmax[i0] = 0;
-        c.vmax[i0] = 0;
+        c.kmax[i0] = c.vmax[i0] = 0;
+        c.kmin[i0] = c.vmin[i0] = kInfBits;
     }
     if (i0 < c.B) {
+        c.wide[i0] = 0;
         c.len[i0] = 0;
         c.seen[i0] = 0;
     }
@@ -232,8 +234,9 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_reset_kernel(Kv4View c, Kv4L
         c.w[u * c.R + i] = 0.0f;
     }
     if (threadIdx.x == 0) {
-        c.kmax[u] = 0;
-        c.vmax[u] = 0;
+        c.kmax[u] = c.vmax[u] = 0;
+        c.kmin[u] = c.vmin[u] = kInfBits;
+        if (u == b * c.Hkv) c.wide[b] = 0;
     }
 }
 
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv
     uint32_t* pars = (is_v ? c.vp : c.kp) + u * c.R * (D / kKv4Group);
     const int sub = lane % LPR;
     const int64_t r0 = blockIdx.x * (int64_t)rows_tile * src.tiles;
-    float big = 0.0f;
+    float big = 0.0f, small = INFINITY;        // of the groups' largest values
     Raw<T> raw[kUnroll];
 #pragma unroll 1
     for (int tile = 0; tile < src.tiles; tile += kUnroll) {
@@ -289,7 +292,9 @@ __global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv
             float2 x[8];
             float mn, mx;
             spread(raw[i], x, mn, mx);
-            big = fmaxf(big, quantize16(x, mn, mx, code, par));
+            const float most = quantize16(x, mn, mx, code, par);
+            big = fmaxf(big, most);
+            if (most > 0.0f) small = fminf(small, most);
             if (row < n) {
                 const int64_t slot = slot0 + row;
                 codes[slot * LPR + sub] = code;
@@ -304,18 +309,30 @@ __global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv
             c.w[u * c.R + slot] = 0.0f;
         }
     }
-    // the CTA's largest value, then one atomic (a maximum does not depend on their order);
+    // the CTA's largest and smallest, then one atomic each (neither depends on their order);
     // a check by every warp made all of them queue at the unit's one word
-    __shared__ float warp_big[kThreadsRows / 32];
+    __shared__ float2 warp_big[kThreadsRows / 32];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-    if (lane == 0) warp_big[warp] = big;
+    for (int o = 16; o > 0; o >>= 1) {
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+        small = fminf(small, __shfl_xor_sync(kFull, small, o));
+    }
+    if (lane == 0) warp_big[warp] = make_float2(big, small);
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < (int)(blockDim.x >> 5); ++i) big = fmaxf(big, warp_big[i]);
-        uint32_t* m = (is_v ? c.vmax : c.kmax) + u;
-        if (big > 0.0f && __float_as_uint(big) > *(volatile uint32_t*)m)
-            atomicMax(m, __float_as_uint(big));
+        for (int i = 1; i < (int)(blockDim.x >> 5); ++i) {
+            big = fmaxf(big, warp_big[i].x);
+            small = fminf(small, warp_big[i].y);
+        }
+        volatile uint32_t *hi = (is_v ? c.vmax : c.kmax) + u, *lo = (is_v ? c.vmin : c.kmin) + u;
+        const bool more = __float_as_uint(big) > *hi, less = __float_as_uint(small) < *lo;
+        if (more) atomicMax((uint32_t*)hi, __float_as_uint(big));
+        if (less) atomicMin((uint32_t*)lo, __float_as_uint(small));
+        if (more || less) {
+            // of two CTAs that bring the one and the other, the later sees both
+            __threadfence();
+            if (kv4_is_wide(__uint_as_float(*lo), __uint_as_float(*hi))) c.wide[b] = 1;
+        }
     }
     if (!src.append) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)

@@ -71,9 +71,9 @@ def normal(L, d, n, G, seed):
             torch.randn(max(n, 1), G, d, generator=g))
 
 
-# (dtype, d, n, G): decode, chunks of few rows, chunks of fp32
+# (dtype, d, n, G): decode, chunks of few rows, chunks of fp32, chunks on the tensor cores
 FORMS = [("bf16", 128, 0, 4), ("bf16", 64, 0, 8), ("f32", 64, 0, 2), ("f32", 128, 0, 8), ("bf16", 128, 4, 2),
-         ("bf16", 64, 8, 1), ("f32", 128, 5, 1), ("f32", 64, 30, 4)]
+         ("bf16", 64, 8, 1), ("f32", 128, 5, 1), ("f32", 64, 30, 4), ("bf16", 128, 5, 4), ("bf16", 64, 70, 2)]
 
 
 @pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 40, 2.0 ** 90])
@@ -153,3 +153,71 @@ def test_a_heavy_token_of_tiny_value_before_a_faint_background(R, dtype, d, n, G
     v[1:] += 0.5
     v[9] *= 2.0 ** 12
     run(R, dtype, d, k, v, Q, n)
+
+
+def test_wide_sequences_among_others(R):
+    """A batch of four: huge values in one sequence from the start, in another by an append; a
+    captured chunk with weights, replayed after the append and after a rebuild without them."""
+    B, Hkv, G, d, n, L = 4, 2, 4, 128, 6, 200
+    lengths = [200, 90, 150, 64]
+    k, v = T.keys((B, Hkv, L, d), 1, "bf16"), T.rand((B, Hkv, L, d), 2, "bf16")
+    k2, v2 = T.keys((B, Hkv, 3, d), 3, "bf16"), T.rand((B, Hkv, 3, d), 4, "bf16")
+    plain = (k.clone(), v.clone())
+    v[1, 1, 3] *= 2.0 ** 50
+    k2[2, 0, 1, 5] = 2.0 ** 40
+    Q = T.rand((B, n, G * Hkv, d), 5, "bf16")
+    Q[2, :, :, 5] = -1.0                                 # no row gives the huge key weight
+    cfg = R.Config(head_dim=d, n_q_heads=G * Hkv, n_kv_heads=Hkv, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, L + 3, B, max_queries=B * n)
+    Qc = Q.cuda()
+    out = torch.empty_like(Qc)
+    kv4.recsa_kv4_build(k.cuda(), v.cuda(), lengths)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            kv4.recsa_kv4_prefill_chunk(Qc, out, accumulate_rows=2)
+
+    def check(units):
+        kv4.weights().zero_()
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        w = T.np64(kv4.weights())
+        for b, row in enumerate(units):
+            for h, u in enumerate(row):
+                u.w[:] = 0
+                for i in range(n):
+                    at = u.seen - n + i
+                    qs = T.np64(Q[b, i, h * G:(h + 1) * G])
+                    want = u.attend(qs, at, accumulate=i >= n - 2)
+                    for x in range(G):
+                        floor = floor_of(u, u.steps, qs[x], at, "bf16", True)
+                        err = np.abs(T.np64(out[b, i, h * G + x]) - want[x])
+                        assert (err <= T.HALF["bf16"] * np.abs(want[x]) * 1.01 + floor).all(), (b, h, i, x)
+                assert abs(w[b, h].sum() - 2 * G) <= 2.0 ** -17 * 2 * G
+                assert np.abs(w[b, h, :len(u.w)] - u.w).max() <= 2.0 ** -9
+
+    def fresh(k, v):
+        units = [[O.Unit(d) for _ in range(Hkv)] for _ in range(B)]
+        for b in range(B):
+            for h in range(Hkv):
+                u, x = units[b][h], T.np64(v[b, h, :lengths[b]])
+                u.append(T.np64(k[b, h, :lengths[b]]), x)
+                u.steps = O.quantize(x)[1]
+        return units
+
+    units = fresh(k, v)
+    check(units)
+    kv4.recsa_kv4_append(k2.cuda(), v2.cuda())
+    for b in range(B):
+        for h in range(Hkv):
+            u = units[b][h]
+            u.append(T.np64(k2[b, h]), T.np64(v2[b, h]))
+            u.steps = np.concatenate([u.steps, O.quantize(T.np64(v2[b, h]))[1]])
+    check(units)
+    kv4.recsa_kv4_build(plain[0].cuda(), plain[1].cuda(), lengths)
+    check(fresh(*plain))
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
