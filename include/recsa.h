@@ -403,7 +403,8 @@ RECSA_API recsa_status recsa_kv4_append(recsa_kv4* kv4, const void* k_new, const
 /* One query per sequence over all its cached tokens.  q, out: [batch][Hq][d] device,
  * 16-byte aligned.  A sequence of length 0 gets zeros.  accumulate != 0: the weight of
  * every slot (per KV head) also grows by the sum over the G query heads of its softmax
- * probability. */
+ * probability.  out may be q itself where no weights accumulate; any other overlap
+ * is RECSA_E_INVAL. */
 RECSA_API recsa_status recsa_kv4_decode(recsa_kv4* kv4, const void* q, void* out,
                                         int32_t accumulate, void* stream);
 
@@ -413,7 +414,8 @@ RECSA_API recsa_status recsa_kv4_decode(recsa_kv4* kv4, const void* q, void* out
  * the cached tokens up to that position.  Rows i >= n_b are neither read nor written.  A
  * count out of range, or above P_b, is recorded as RECSA_E_DEVICE and its rows are skipped.
  * A row that sees no token gets zeros.  accumulate_rows: the newest that many rows of each
- * sequence add to the weights as recsa_kv4_decode does (0: none).
+ * sequence add to the weights as recsa_kv4_decode does (0: none).  O may be Q itself as in
+ * recsa_kv4_decode.
  * Keys and values may span any magnitudes.  A bf16 chunk of more than 8 rows a KV head takes a
  * far slower form for a sequence in which one group's largest |value| since the last build is
  * more than 2^24 times another's (groups of zeros aside). */

@@ -25,6 +25,13 @@ struct Kv4Layout {
 bool chunk_on_tensor_cores(int dtype, int rows) { return dtype == RECSA_BF16 && rows > 8; }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+// May a call read its queries from q and write its rows to out, `bytes` each?  In place, yes,
+// unless a second launch reads the queries again (for weights); a partial overlap, never.
+bool apart(const void* q, const void* out, size_t bytes, bool again) {
+    const uintptr_t a = (uintptr_t)q, b = (uintptr_t)out;
+    if (a == b) return !again;
+    return a < b ? b - a >= bytes : a - b >= bytes;
+}
 bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 recsa_status kv4_layout(const recsa_config* c, int64_t cap, int B, int Qmax, Kv4Layout* L) {
@@ -287,6 +294,8 @@ recsa_status recsa_kv4_decode(recsa_kv4* t, const void* q, void* out, int32_t ac
                               void* stream) {
     if (!t || !q || !out) return RECSA_E_INVAL;
     if (!on16(q) || !on16(out)) return RECSA_E_INVAL;
+    const size_t bytes = (size_t)t->c.B * t->c.Hq * t->L.D * t->L.esize;
+    if (!apart(q, out, bytes, accumulate != 0)) return RECSA_E_INVAL;
     Kv4Query qv = {};
     qv.q = q;
     qv.out = out;
@@ -305,6 +314,8 @@ recsa_status recsa_kv4_prefill_chunk(recsa_kv4* t, const void* Q, int32_t n, con
                                      void* O, int32_t accumulate_rows, void* stream) {
     if (!t || !Q || !O || n < 1 || accumulate_rows < 0) return RECSA_E_INVAL;
     if (!on16(Q) || !on16(O) || ((uintptr_t)counts & 3u)) return RECSA_E_INVAL;
+    const size_t bytes = (size_t)t->c.B * n * t->c.Hq * t->L.D * t->L.esize;
+    if (!apart(Q, O, bytes, accumulate_rows != 0)) return RECSA_E_INVAL;
     OnDevice on(t->device);
     if (!on.ok) return RECSA_E_CUDA;
     const cudaStream_t s = (cudaStream_t)stream;

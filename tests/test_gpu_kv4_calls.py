@@ -27,3 +27,33 @@ def test_outputs_belong_to_the_stream_of_the_call(R, counts):
     assert all(torch.equal(x, y) for x, y in zip(r_out, r_want))
     if counts:
         assert (out[0, 5:] == 0).all() and (out[0, :5] != 0).any() and (out[1] != 0).any()
+
+
+@pytest.mark.parametrize("dtype,d,G,n", [("bf16", 128, 4, 40), ("bf16", 64, 2, 3), ("f32", 64, 4, 9), ("f32", 128, 1, 1)])
+def test_rows_in_place(R, dtype, d, G, n):
+    """out = q is right without weights, over cut and whole units; with weights a second launch
+    would read the overwritten queries, and the call is refused, as any partial overlap is."""
+    B, Hkv = 2, 2
+    kv4, _ = T.make(R, dtype, d, Hkv, G, [900, 64], max_queries=B * max(n // 2, 1))
+    Q = T.rand((B, n, G * Hkv, d), 5, dtype).cuda()
+    want = kv4.prefill(Q)
+    X = Q.clone()
+    kv4.recsa_kv4_prefill_chunk(X, X)
+    assert torch.equal(X, want)
+    q = Q[:, 0].contiguous()
+    want, x = kv4.decode(q), q.clone()
+    kv4.recsa_kv4_decode(x, x)
+    assert torch.equal(x, want)
+    flat = torch.zeros(q.numel() + 64, dtype=q.dtype, device="cuda")
+    a, b = (flat[i:i + q.numel()].view_as(q) for i in (0, 64))
+    for args, kw in [((q, q), dict(accumulate=True)), ((a, b), {}), ((b, a), {})]:
+        with pytest.raises(R.RecsaError) as e:
+            kv4.recsa_kv4_decode(*args, **kw)
+        assert e.value.status == R.RECSA_E_INVAL
+    flat = torch.zeros(Q.numel() + 64, dtype=q.dtype, device="cuda")
+    a, b = (flat[i:i + Q.numel()].view_as(Q) for i in (0, 64))
+    for args, kw in [((Q, Q), dict(accumulate_rows=1)), ((a, b), {}), ((b, a), {})]:
+        with pytest.raises(R.RecsaError) as e:
+            kv4.recsa_kv4_prefill_chunk(*args, **kw)
+        assert e.value.status == R.RECSA_E_INVAL
+    assert (kv4.weights() == 0).all()
