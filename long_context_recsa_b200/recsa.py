@@ -463,11 +463,12 @@ class RecsaKV4:
                                  f"{tuple(t.shape)}")
         if len(lens) != self.batch or max(lens) > min(k.shape[2], v.shape[2]):
             raise ValueError(f"lengths {lens}: {self.batch} of them, at most the rows given")
-        if k.stride() != v.stride():
-            raise ValueError("k and v must have the same strides")
         arr = (ctypes.c_int64 * self.batch)(*lens)
         # a dim of one element has no stride that matters: the library checks all three
-        st = [s if n > 1 else c.head_dim for s, n in zip(k.stride()[:3], k.shape[:3])]
+        st, st_v = ([s if n > 1 else c.head_dim for s, n in zip(t.stride()[:3], t.shape[:3])]
+                    for t in (k, v))
+        if st != st_v:
+            raise ValueError("k and v must have the same strides")
         strides = (ctypes.c_int64 * 3)(*st)
         _check(lib.recsa_kv4_build(self.handle, k.data_ptr(), v.data_ptr(), strides, arr,
                                    self._on(stream)), "recsa_kv4_build")

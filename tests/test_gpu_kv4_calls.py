@@ -57,3 +57,20 @@ def test_rows_in_place(R, dtype, d, G, n):
             kv4.recsa_kv4_prefill_chunk(*args, **kw)
         assert e.value.status == R.RECSA_E_INVAL
     assert (kv4.weights() == 0).all()
+
+
+@pytest.mark.parametrize("lengths", [[7], [1]])
+def test_strides_of_dims_of_one_element_do_not_matter(R, lengths):
+    """k alone and v a part of a larger tensor, one sequence and one KV head: the same rows."""
+    d, L = 64, lengths[0]
+    cfg = R.Config(head_dim=d, n_q_heads=2, n_kv_heads=1, dtype="bf16")
+    k = T.keys((1, 1, L, d), 1, "bf16").cuda()
+    big = T.rand((3, 2, L, d), 2, "bf16").cuda()
+    v = big[1:2, 1:2]
+    assert k.stride() != v.stride()
+    kv4, same = R.RecsaKV4(cfg, 16, 1), R.RecsaKV4(cfg, 16, 1)
+    kv4.recsa_kv4_build(k, v, lengths)
+    same.recsa_kv4_build(k, v.clone(memory_format=torch.contiguous_format), lengths)
+    assert all(torch.equal(a, b) for a, b in zip(kv4.read(0, L), same.read(0, L)))
+    with pytest.raises(ValueError):
+        kv4.recsa_kv4_build(k.expand(1, 1, L, d), T.rand((1, 1, L, 2 * d), 3, "bf16").cuda()[..., :d], [2])
