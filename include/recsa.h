@@ -394,8 +394,10 @@ RECSA_API recsa_status recsa_kv4_build(recsa_kv4* kv4, const void* k, const void
 /* Append tokens: k_new, v_new are device arrays [batch][Hkv][n][d] (contiguous, 16-byte
  * aligned), n >= 1.  counts: optional device int32 [batch], 0 <= counts[b] <= n: only the
  * first counts[b] rows of sequence b are appended (the rest is not read).  New rows have
- * weight 0.  A sequence that would pass the capacity is left unchanged and the status
- * word records RECSA_E_CAPACITY; a count out of range is taken as 0 and recorded as
+ * weight 0.  A sequence that would pass the capacity, or 2^31 - 1 tokens in all since
+ * its last build (positions are int32, evicted tokens count), is left unchanged and the status
+ * word records RECSA_E_CAPACITY; the lengths and tokens_seen of recsa_kv4_info tell the two
+ * apart, and a build starts the positions anew.  A count out of range is taken as 0 and recorded as
  * RECSA_E_DEVICE. */
 RECSA_API recsa_status recsa_kv4_append(recsa_kv4* kv4, const void* k_new, const void* v_new,
                                         int32_t n, const int32_t* counts, void* stream);

@@ -74,3 +74,24 @@ def test_strides_of_dims_of_one_element_do_not_matter(R, lengths):
     assert all(torch.equal(a, b) for a, b in zip(kv4.read(0, L), same.read(0, L)))
     with pytest.raises(ValueError):
         kv4.recsa_kv4_build(k.expand(1, 1, L, d), T.rand((1, 1, L, 2 * d), 3, "bf16").cuda()[..., :d], [2])
+
+
+def test_append_up_to_the_last_position(R):
+    """2^31 - 1 tokens a sequence in all: the last positions are used, one more is refused and
+    leaves the sequence as it was, and a build starts anew."""
+    kv4, _ = T.make(R, "f32", 64, 1, 1, [4, 4], cap=12)
+    seen = kv4._table(kv4.workspace, kv4.info.tokens_seen, (2,), torch.int64)
+    seen[0] = 2 ** 31 - 1 - 3                            # as after as many appends and evictions
+    k = T.rand((2, 1, 3, 64), 1, "f32").cuda()
+    kv4.recsa_kv4_append(k, k)
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+    assert kv4.positions()[0, 0, 4:7].tolist() == [2 ** 31 - 4, 2 ** 31 - 3, 2 ** 31 - 2]
+    q = T.rand((2, 1, 1, 64), 2, "f32").cuda()
+    both = kv4.prefill(q)
+    assert torch.equal(both[0, 0], kv4.decode(q[:, 0].contiguous())[0])
+    kv4.recsa_kv4_append(k[:, :, :1].contiguous(), k[:, :, :1].contiguous())
+    assert kv4.recsa_kv4_get_status() == R.RECSA_E_CAPACITY
+    assert kv4.lengths().tolist() == [7, 8] and seen.tolist() == [2 ** 31 - 1, 8]
+    kv4.recsa_kv4_build(k, k, [3, 3])
+    kv4.recsa_kv4_append(k, k)
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK and seen.tolist() == [6, 6]
