@@ -13,6 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "librecsa.so")
+BUILD = os.path.join(HERE, "_build")
 SOURCES = ["recsa_api.cu", "tree_kernels.cu", "select_attend.cu", "prefill_tc.cu", "noalloc.cu",
            "gated.cu", "offload.cu", "kv4_api.cu", "kv4_rows.cu", "kv4_attend.cu",
            "kv4_chunk.cu", "kv4_evict.cu"]
@@ -56,16 +57,21 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     deps = [os.path.join(CSRC, s) for s in SOURCES]
     deps += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     deps.append(os.path.join(HERE, "..", "include", "recsa.h"))
-    if not force and not _stale(out, deps):
-        return out
-    # one object per source, compiled side by side; an object newer than every file it
-    # was compiled from (listed in its .d file) is kept
-    objdir = os.path.join(HERE, "_build", "bounds" if debug_bounds else "release")
-    os.makedirs(objdir, exist_ok=True)
     flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
              "-Xcompiler", "-fvisibility=hidden"]
     if debug_bounds:
         flags.append("-DRECSA_DEBUG_BOUNDS")
+    # one object per source, compiled side by side; an object newer than every file it
+    # was compiled from (listed in its .d file), and made with the same flags, is kept
+    objdir = os.path.join(BUILD, "bounds" if debug_bounds else "release")
+    made_with, now = os.path.join(objdir, "flags.txt"), "\n".join([*flags, *SOURCES])
+    if not os.path.exists(made_with) or open(made_with).read() != now:
+        force = True
+    if not force and not _stale(out, deps):
+        return out
+    os.makedirs(objdir, exist_ok=True)
+    if force and os.path.exists(made_with):
+        os.remove(made_with)             # until all objects are made anew
     if verbose:
         flags.append("-Xptxas=-v")
 
@@ -84,6 +90,8 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
         objs = list(pool.map(compile_one, SOURCES))
     subprocess.run([nvcc_path(), *ARCH, "-shared", "-o", out + ".tmp", *objs], check=True)
     os.replace(out + ".tmp", out)
+    with open(made_with, "w") as f:
+        f.write(now)
     return out
 
 
