@@ -123,6 +123,37 @@ inline cudaError_t kv4_launch(void (*kern)(P...), dim3 grid, int threads, size_t
 __device__ __forceinline__ float kv4_step(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float kv4_off(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// 2^x.  (Without .ftz every call is wrapped in the scaling of subnormal results.)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^e for a whole e, clamped to the normal range.
+__device__ __forceinline__ float pow2i(int e) {
+    e = e < -126 ? -126 : e > 127 ? 127 : e;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ int exponent_of(float x) {   // floor(log2 |x|), -127 for 0
+    return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(y))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return y;
+}
+
 // Groups of keys or values from `least` to `most` in size: more than fp16 holds, scaled by `most`
 // to 2^13?  (2^-24 of it is 2^-11 there, off by 2^-14 of itself; below, bits are lost.)
 constexpr float kKv4Wide = 0x1p-24f;

@@ -162,20 +162,6 @@ struct Centre {
         return y;
     }
 };
-// (without .ftz every call is wrapped in the scaling of subnormal results)
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// 2^e for a whole e, clamped to the normal range.
-__device__ __forceinline__ float pow2i(int e) {
-    e = e < -126 ? -126 : e > 127 ? 127 : e;
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-__device__ __forceinline__ int exponent_of(float x) {   // floor(log2 |x|), -127 for 0
-    return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
-}
 
 // The largest P' of a lane: fp16 pairs as integers (no P' is negative), fp32 tensors' high parts.
 template <int T>

@@ -275,29 +275,6 @@ __device__ __forceinline__ void ld16(uint32_t t, uint32_t (&u)[16]) {
         : "r"(t)
         : "memory");
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-          "l"(reinterpret_cast<uint64_t&>(c)));
-    return y;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 y;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-    return y;
-}
-
-// (without .ftz every call is wrapped in the scaling of subnormal results)
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // ---- softmax of 32 scores of a row ----
 // Scores of tokens behind position lim become -infinity, in TMEM.  (Not inlined: the few
@@ -422,13 +399,6 @@ __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-__device__ __forceinline__ float pow2i(int e) {   // 2^e, clamped to the normal range
-    e = e < -126 ? -126 : e > 127 ? 127 : e;
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-__device__ __forceinline__ int exponent_of(float x) {
-    return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
-}
 
 // Place of a 16-byte chunk (8 dims) of a row: slabs of 64 dims, swizzled.
 __device__ __forceinline__ uint32_t chunk_of(int row, int ch) {

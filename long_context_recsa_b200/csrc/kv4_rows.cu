@@ -85,22 +85,6 @@ __device__ __forceinline__ void spread(const Raw<float>& r, float2 (&x)[8], floa
     mx = -min_nan(hi, __shfl_xor_sync(kFull, hi, 1));
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 y;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-    return y;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t&>(y))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-          "l"(reinterpret_cast<uint64_t&>(c)));
-    return y;
-}
 __device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
 
 // bf16 bits (in the high half) of the largest bf16 <= x.
