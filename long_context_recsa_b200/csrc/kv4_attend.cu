@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         auto fetch = [&](int tile, int s) {
             unsigned char* st = my_ring + s * St::kBytes;
             uint64_t* bar = &bars[warp][s];
-            const int64_t r = (int64_t)tile * kTile;
+            int64_t r = (int64_t)tile * kTile;
+            if (!in_bounds(r >= 0 && r + kTile <= c.R, c.status)) r = 0;
             mbar_expect_tx(bar, 2 * St::kCodes + 2 * St::kPars + (CHUNK ? kTile * 4 : 0));
             tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
             tma_rows(st + St::kV, &maps.v, (int)r, u, bar);
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         const bool whole = cta0 == cta1;
         auto store_row = [&](int r, int d4, float4 v, float mx, float ls) {
             const int row = row0 + r;
-            if (row >= row_end) return;
+            if (row >= row_end || !in_bounds(row < qv.n * c.G && row - row0 < RB, c.status)) return;
             const float inv = ls > 0.0f || ls != ls ? 1.0f / ls : 0.0f;
             const int i = row / c.G, gg = row % c.G;
             TI* o = reinterpret_cast<TI*>(qv.out) +
@@ -822,7 +823,10 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
             }
             if (d4 == 0) sc_.stat[(int64_t)u * qv.w * c.G + row - qv.i0 * c.G] = kv4_stat(mx, ls);
         };
-        auto slot = [&](int64_t cta) { return 2 * cta + (cta == cta0 ? 1 : 0); };
+        auto slot = [&](int64_t cta) {
+            if (!in_bounds(cta >= 0 && cta < gridDim.x, c.status)) cta = 0;
+            return 2 * cta + (cta == cta0 ? 1 : 0);
+        };
         auto part_of = [&](int64_t cta) { return sc_.part + (size_t)slot(cta) * RB * (D + 2); };
         float* part = whole ? nullptr : part_of(blockIdx.x);
         const int nr = row_end - row0 < RB ? row_end - row0 : RB;   // rows of the block that are there
@@ -1007,7 +1011,8 @@ __global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_ke
         auto fetch = [&](int tile, int s) {
             unsigned char* st = my_ring + s * St::kBytes;
             uint64_t* bar = &bars[warp][s];
-            const int64_t r = (int64_t)tile * kTile;
+            int64_t r = (int64_t)tile * kTile;
+            if (!in_bounds(r >= 0 && r + kTile <= c.R, c.status)) r = 0;
             mbar_expect_tx(bar, St::kCodes + St::kPars + ((CHUNK ? 1 : 0) + (SUMS ? 0 : 1)) * kTile * 4);
             tma_rows(st + St::kK, &maps.k, (int)r, u, bar);
             if (!SUMS) bulk_g2s(st + St::kW, c.w + u * c.R + r, kTile * 4, bar);
@@ -1017,6 +1022,7 @@ __global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_ke
         const int64_t unit0 = at - tile0;              // first tile of the unit in the list
         const int64_t cta0 = unit0 / quota, cta1 = (unit0 + tiles - 1) / quota;
         auto cut_stat = [&](int64_t cta) {
+            if (!in_bounds(cta >= 0 && cta < gridDim.x, c.status)) cta = 0;
             return reinterpret_cast<float2*>(sc_.part) + (2 * cta + (cta == cta0 ? 1 : 0)) * n_blocks * RB;
         };
         int mine = L > 0 && row0 < row_end ? (tile1 - tile0 - base + step - 1) / step : 0;
@@ -1130,14 +1136,14 @@ __global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_ke
                     // this warp's alone: what the tile brought, and more
                     const float* old = reinterpret_cast<const float*>(st + St::kW) + r0 + g;
                     float* w = c.w + u * c.R + tok;
-                    if (tok < L) w[0] = old[0] + sum0;
-                    if (tok + 8 < L) w[8] = old[8] + sum1;
+                    if (tok < L && in_bounds(tok < c.cap, c.status)) w[0] = old[0] + sum0;
+                    if (tok + 8 < L && in_bounds(tok + 8 < c.cap, c.status)) w[8] = old[8] + sum1;
                 }
             }
             if (spread && !SUMS) {
                 __syncthreads();
                 const int64_t tok = (int64_t)tile * kTile + lane;
-                if (warp == 0 && alive && tok < L) {
+                if (warp == 0 && alive && tok < L && in_bounds(tok < c.cap, c.status)) {
                     float x = reinterpret_cast<const float*>(st + St::kW)[lane];
 #pragma unroll
                     for (int i = 0; i < kAttendWarps; ++i) x += sums[i][lane];
@@ -1164,6 +1170,7 @@ __global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_ke
                     const float2 p = stat[k * n_blocks * RB + i];
                     l = fmaf(p.y, ex2(p.x - m), l);
                 }
+                if (!in_bounds(row0 + i - qv.i0 * c.G < qv.w * c.G, c.status)) continue;
                 if (cta0 == cta1)
                     sc_.stat[(int64_t)u * qv.w * c.G + row0 + i - qv.i0 * c.G] = kv4_stat(m, l);
                 else

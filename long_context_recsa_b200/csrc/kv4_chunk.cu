@@ -735,8 +735,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 }
             }
             if ((TWO || stream == 0) && some && ok) {
-                const bool live = row < un.row_end;
                 const int i = row / c.G, g = row % c.G, rr = row - un.row0;
+                const bool live = row < un.row_end && in_bounds(row < qv.n * c.G && rr < RB, c.status);
                 const bool any = l > 0.0f || l != l;
                 const float inv = any ? pow2i(ev - 13) / l : 0.0f;
                 float* part = sc.part + (size_t)(2 * blockIdx.x + (un.tile0 == 0 ? 1 : 0)) * RB * (D + 2);
@@ -797,7 +797,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             const float scale = pow2i(13 - exponent_of(__uint_as_float((is_v ? c.vmax : c.kmax)[u])));
             auto fetch = [&](int t) {
                 const uint32_t n = n_tiles + t;
-                const int64_t row = u * c.R + (int64_t)(tile0 + t) * kTok;
+                int64_t row = u * c.R + (int64_t)(tile0 + t) * kTok;
+                if (!in_bounds(tile0 + t >= 0 && (int64_t)(tile0 + t + 1) * kTok <= c.R, c.status)) row = 0;
                 unsigned char* raw = raw_at(n);
                 uint64_t* bar = &bars.raw_full[is_v][n & (deep - 1)];
                 if (is_v) {
@@ -1046,6 +1047,7 @@ __global__ void __launch_bounds__(256, 3) kv4_join_kernel(const __grid_constant_
     const int row = qv.i0 * c.G + rel + lane;
     if (row >= w_end * c.G) return;
     auto part = [&](int64_t cta) {
+        if (!in_bounds(cta >= 0 && cta < ctas && rr < RB, c.status)) cta = 0;
         return sc.part + (size_t)(2 * cta + (cta == cta0 ? 1 : 0)) * RB * (D + 2);
     };
     float m = kKv4MinLog2, l = 0.0f;

@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv4_evict_kernel(Kv4View c, int
             seen += __popc(m);
             const bool fr = i < lo_end && !kept, mv = i >= lo_end && kept;
             const uint32_t mf = __ballot_sync(kFull, fr), mm = __ballot_sync(kFull, mv);
-            if (fr) free_list[free0 + __popc(mf & below)] = (int32_t)(seg0 + i);
-            if (mv) move_list[move0 + __popc(mm & below)] = (int32_t)(seg0 + i);
+            const int at_f = free0 + __popc(mf & below), at_m = move0 + __popc(mm & below);
+            if (fr && in_bounds(at_f >= 0 && at_f < c.R / 2, c.status)) free_list[at_f] = (int32_t)(seg0 + i);
+            if (mv && in_bounds(at_m >= 0 && at_m < c.R / 2, c.status)) move_list[at_m] = (int32_t)(seg0 + i);
             free0 += __popc(mf);
             move0 += __popc(mm);
         }
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv4_evict_kernel(Kv4View c, int
              x += CS * kEvictThreads) {
             const int j = (int)(x / CH), p = (int)(x % CH);
             const int64_t to = __ldcg(free_list + j), from = __ldcg(move_list + j);
+            if (!in_bounds(to >= 0 && to < budget && from >= budget && from < L, c.status)) continue;
             if (p < CK) {
                 kc[to * CK + p] = kc[from * CK + p];
             } else if (p < 2 * CK) {

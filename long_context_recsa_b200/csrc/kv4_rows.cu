@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv
             const float most = quantize16(x, mn, mx, code, par);
             big = fmaxf(big, most);
             if (most > 0.0f) small = fminf(small, most);
-            if (row < n) {
-                const int64_t slot = slot0 + row;
+            const int64_t slot = slot0 + row;
+            if (row < n && in_bounds(slot >= 0 && slot < c.cap, c.status)) {
                 codes[slot * LPR + sub] = code;
                 if ((sub & 1) == 0) pars[slot * (D / kKv4Group) + (sub >> 1)] = par;
             }
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreadsRows, 4) kv4_rows_kernel(Kv4View c, Kv
     if (!is_v) {
         for (int64_t i = r0 + threadIdx.x; i < r0 + rows_tile * src.tiles && i < n; i += blockDim.x) {
             const int64_t slot = slot0 + i;
+            if (!in_bounds(slot >= 0 && slot < c.cap, c.status)) continue;
             c.pos[u * c.R + slot] = (int32_t)(pos0 + i);
             c.w[u * c.R + slot] = 0.0f;
         }
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThreadsRows) kv4_read_kernel(Kv4View c, int64
     for (int i = 0; i < kReadRows; ++i) {
         const int64_t slot = start + r + i * RPW;
         code[i] = par[i] = 0;
-        if (r + i * RPW < n && slot < L) {
+        if (r + i * RPW < n && slot < L && in_bounds(slot >= 0 && slot < c.cap, c.status)) {
             code[i] = codes[slot * (D / 8) + sub];
             par[i] = pars[slot * (D / kKv4Group) + (sub >> 2)];
         }
