@@ -134,6 +134,7 @@ __device__ __forceinline__ float pow2i(int e) {
     e = e < -126 ? -126 : e > 127 ? 127 : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
+__device__ __forceinline__ float pow2z(int e) { return e < -126 ? 0.0f : pow2i(e); }
 __device__ __forceinline__ int exponent_of(float x) {   // floor(log2 |x|), -127 for 0
     return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
 }

@@ -28,7 +28,11 @@
 // fp16, off by at most 2^-11 relative, less than bf16's own 2^-8 of the output.  fp32 tensors
 // use two fp16 columns a row for q and for P' (high and low part, 22 bits; the low part of P'
 // is scaled by 2^11, so that it keeps its bits where P' itself is below fp16's normal range).
-// The softmax maximum, its sum and all accumulators are fp32.
+// The softmax maximum, its sum and all accumulators are fp32.  The products' own accumulators do
+// not round to nearest: summed up in them, the codes' share drifts, and what is left beside the
+// offsets' share may be a thousandth of it (16 sequences of 524288 x 16 KV heads in bf16: 3.1e-3
+// of the output instead of 1.67e-3; fp32, 700000 tokens: 2e-4 instead of 2e-6).  So each
+// product's result is added to O, which costs 4 x 524288 12 us of 711.
 //
 // Each row and group of dims has its own scale of P' (`up`): p s may span any range, and what
 // falls below fp16 is less than 2^-30 of the row's and group's largest p s so far.  So a huge
@@ -65,7 +69,7 @@ constexpr int kStagesKv4 = 2;
 constexpr int kGridMax = 148 * 4;
 constexpr int kJoin = 16;            // partial results that one CTA joins
 constexpr float kSlack = 6.0f;       // p may reach 2^6 before the running maximum moves
-constexpr float kMostUp = 0x1p120f;  // largest scale of P', and the first
+constexpr int kMostUpLog2 = 120;     // largest scale of P' (a power of two), and the first
 constexpr int kMostLog2 = 14;        // P' moves its scale where it passes 2^14 ..
 constexpr float kSetUp = 0x1p-8f;    // .. which is set so that the largest P' is 2^5 to 2^6
 constexpr float kLowUp = 2048.0f;    // fp32 tensors: scale of the low part of P' (its own column)
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
         __syncthreads();
 
         float O[NCS][NG][2][4], bias[NCS][RL][NG], m[NCS][RL], l[NCS][RL], rsc[NCS][RL];
-        float up[NCS][RL][NG];                         // of P': O is `up` times the sum of p s code
+        float up[NCS][RL][NG];                         // O is `up` (2^e) times the sum of p s code
         int lim[NCS][RL];
 #pragma unroll
         for (int cs = 0; cs < NCS; ++cs) {
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     bias[cs][e][j] = 0.0f;
-                    up[cs][e][j] = kMostUp;
+                    up[cs][e][j] = pow2i(kMostUpLog2);
                 }
             }
         }
@@ -612,8 +616,10 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                             x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                            const float mn = fmaxf(m[cs][e], x);
-                            const float f = ex2(m[cs][e] - mn), inv = __fdividef(1.0f, f);
+                            // by a whole number, so that every scaling below is exact
+                            const float mn = fmaxf(m[cs][e], ceilf(x));
+                            const int k = (int)fminf(mn - m[cs][e], 1000.0f);
+                            const float f = pow2z(-k);
                             m[cs][e] = mn;
                             if (empty) continue;
                             l[cs][e] *= f;
@@ -621,10 +627,9 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                             for (int j = 0; j < NG; ++j) {
                                 bias[cs][e][j] *= f;
                                 // O falls by f as a sum: its scale rises, O stays, up to a limit
-                                const float y = up[cs][e][j] * inv;
-                                if (!(y <= kMostUp))
-                                    scale_row<T>(O[cs][j], e, __fdividef(f * kMostUp, up[cs][e][j]));
-                                up[cs][e][j] = y <= kMostUp ? y : kMostUp;
+                                const int y = exponent_of(up[cs][e][j]) + k;
+                                if (y > kMostUpLog2) scale_row<T>(O[cs][j], e, pow2z(kMostUpLog2 - y));
+                                up[cs][e][j] = pow2i(y < kMostUpLog2 ? y : kMostUpLog2);
                             }
                         }
                 }
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         const float most = __shfl_sync(kFull, y[i % NE], from + t);
                         if (up[cs][e][j] > most) {
                             const float x = most * kSetUp;
-                            scale_row<T>(O[cs][j], e, __fdividef(x, up[cs][e][j]));
+                            scale_row<T>(O[cs][j], e, pow2z(exponent_of(x) - exponent_of(up[cs][e][j])));
                             up[cs][e][j] = x;
                         }
                     }
@@ -736,8 +741,14 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                                 bias[cs][e][j] = fmaf(sc[cs][2 * e], c0,
                                                       fmaf(sc[cs][2 * e + 1], c1, bias[cs][e][j]));
                             const uint32_t x0 = movm(b0[cs][j]), x1 = movm(b1[cs][j]);
-                            mma16816(O[cs][j][0], a0, a1, a2, a3, x0, x1);
-                            mma16816(O[cs][j][1], a4, a5, a6, a7, x0, x1);
+                            float acc[2][4];
+                            mma16816_0(acc[0], a0, a1, a2, a3, x0, x1);
+                            mma16816_0(acc[1], a4, a5, a6, a7, x0, x1);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                O[cs][j][0][z] += acc[0][z];
+                                O[cs][j][1][z] += acc[1][z];
+                            }
                         }
                     }
                 }
@@ -795,7 +806,7 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
                         v.z = fmaf(O[cs][j][1][1], 1.0f / kLowUp, O[cs][j][1][0]);
                         v.w = fmaf(O[cs][j][1][3], 1.0f / kLowUp, O[cs][j][1][2]);
                     }
-                    const float down = __fdividef(1.0f, up[cs][e][j]);
+                    const float down = pow2i(-exponent_of(up[cs][e][j]));
                     v.x = fmaf(v.x, down, bs);
                     v.y = fmaf(v.y, down, bs);
                     v.z = fmaf(v.z, down, bs);

@@ -221,3 +221,47 @@ def test_wide_sequences_among_others(R):
     kv4.recsa_kv4_build(plain[0].cuda(), plain[1].cuda(), lengths)
     check(fresh(*plain))
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+@pytest.mark.parametrize("d,G,n,L", [(64, 8, 0, 2_000_001), (64, 8, 16, 500_000), (128, 4, 24, 300_003)])
+def test_fp32_sums_over_a_long_cache_do_not_drift(R, d, G, n, L):
+    """Nearly flat softmax over many tokens: the output is a small mean of values of both signs, so
+    a sum that rounds one way shows (2e-5 to 2e-4 of the output, in norm, with the products' own
+    accumulators).  Errors that differ from token to token shrink as the output does: scores
+    16 * 2^-24 * 4, exp2 2^-22 and P' 2^-22, together below 2^-19; a lane's m additions to nearest
+    add 2^-24 sqrt(m), m <= 2000 (2^-18.5): 2^-18 in norm.  The oracle takes the cache's values as
+    they are read back (exact in fp32, tested beside this file)."""
+    k, v, Q = normal(L, d, n, G, 8)
+    cfg = R.Config(head_dim=d, n_q_heads=G, n_kv_heads=1, dtype="f32")
+    kv4 = R.RecsaKV4(cfg, L, 1, max_queries=max(n, 1))
+    kv4.recsa_kv4_build(k.cuda()[None, None], v.cuda()[None, None], [L])
+    out = kv4.prefill(Q[None].cuda())[0] if n else kv4.decode(Q.cuda())
+    K, V = (x[0, 0].double() for x in kv4.read(0, L))
+    at = torch.arange(L, device="cuda")
+    off = size = 0.0
+    for i in range(max(n, 1)):
+        s = Q[i].cuda().double() @ K.T / d ** 0.5
+        want = torch.softmax(s.masked_fill(at > L - max(n, 1) + i, -float("inf")), -1) @ V
+        off += float((out[i].double() - want).square().sum())
+        size += float(want.square().sum())
+    assert off ** 0.5 <= 2.0 ** -18 * size ** 0.5, (off / size) ** 0.5
+
+
+def test_bf16_sums_over_a_long_cache_do_not_drift(R):
+    """512 units of 262144 tokens (one pair of tensors read by all: strides of 0), nearly flat
+    softmax: beside the outputs' own rounding, P' may be off by 2^-11 independently."""
+    B, Hkv, G, d, L = 64, 8, 1, 64, 262144
+    k, v, Q = normal(L, d, 0, B * Hkv * G, 9)
+    k, v, Q = k.bfloat16().cuda(), v.bfloat16().cuda(), Q[0].bfloat16().view(B, Hkv * G, d).cuda()
+    cfg = R.Config(head_dim=d, n_q_heads=G * Hkv, n_kv_heads=Hkv, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, L, B)
+    kv4.recsa_kv4_build(k.expand(B, Hkv, L, d), v.expand(B, Hkv, L, d), [L] * B)
+    out = kv4.decode(Q).double()
+    u = O.Unit(d)
+    u.append(T.np64(k), T.np64(v))
+    K, V = torch.from_numpy(u.k).cuda(), torch.from_numpy(u.v).cuda()
+    want = torch.softmax(Q.double().view(-1, d) @ K.T / d ** 0.5, -1) @ V
+    want = want.view_as(out)
+    own = (want.bfloat16().double() - want).norm()
+    assert (out - want).norm() <= (own.square() + (2.0 ** -11 * want.norm()).square()).sqrt()
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
