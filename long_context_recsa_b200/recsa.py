@@ -420,7 +420,7 @@ class RecsaKV4:
 
     def __del__(self):
         h = getattr(self, "handle", None)
-        if h is not None and h.value:
+        if h is not None and h.value and lib is not None:   # None while the interpreter ends
             lib.recsa_kv4_free(h)
             self.handle = None
 

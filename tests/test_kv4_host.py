@@ -107,3 +107,12 @@ def test_null_handles_refuse(R):
                        ("recsa_kv4_get_status", (None, None)), ("recsa_kv4_info", (None, None)),
                        ("recsa_kv4_free", (None,))]:
         assert getattr(lib, name)(*args) == R.RECSA_E_INVAL, name
+
+
+def test_a_handle_that_outlives_the_module_is_dropped_quietly(R, monkeypatch):
+    """At the interpreter's end a module's names may be None before the last handle goes."""
+    kv4 = R.RecsaKV4.__new__(R.RecsaKV4)
+    kv4.handle = ctypes.c_void_p(1)
+    monkeypatch.setattr(R, "lib", None)
+    kv4.__del__()
+    kv4.handle = None
