@@ -95,3 +95,67 @@ def test_append_up_to_the_last_position(R):
     kv4.recsa_kv4_build(k, k, [3, 3])
     kv4.recsa_kv4_append(k, k)
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK and seen.tolist() == [6, 6]
+
+
+@pytest.mark.parametrize("dtype,d,G,n", [("bf16", 128, 4, 40), ("bf16", 64, 2, 3), ("f32", 64, 4, 9)])
+def test_a_chunk_without_rows(R, dtype, d, G, n):
+    """Counts of zero for every sequence: nothing is read, written or recorded."""
+    kv4, _ = T.make(R, dtype, d, 2, G, [90, 0], max_queries=2 * n)
+    Q = T.rand((2, n, 2 * G, d), 1, dtype).cuda()
+    out = torch.full_like(Q, 3.0)
+    kv4.recsa_kv4_prefill_chunk(Q, out, torch.zeros(2, dtype=torch.int32, device="cuda"), accumulate_rows=n)
+    assert (out == 3.0).all() and (kv4.weights() == 0).all()
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,d,G,n", [("bf16", 128, 4, 40), ("bf16", 64, 2, 3), ("f32", 64, 4, 9), ("f32", 128, 1, 5)])
+def test_a_query_that_is_no_number_reaches_its_own_row_only(R, dtype, d, G, n, bad):
+    kv4, _ = T.make(R, dtype, d, 2, G, [300, 77], max_queries=2 * n)
+    Q = T.rand((2, n, 2 * G, d), 1, dtype).cuda()
+    want, q = kv4.prefill(Q), Q[:, 0].contiguous()
+    d_want = kv4.decode(q)
+    X = Q.clone()
+    X[1, n // 2, 1, 3] = bad
+    out = kv4.prefill(X)
+    assert torch.isnan(out[1, n // 2, 1]).all()
+    out[1, n // 2, 1] = want[1, n // 2, 1]
+    assert torch.equal(out, want)
+    x = q.clone()
+    x[0, 0, 5] = bad
+    out = kv4.decode(x)
+    assert torch.isnan(out[0, 0]).all()
+    out[0, 0] = d_want[0, 0]
+    assert torch.equal(out, d_want)
+
+
+def test_many_heads_of_a_short_cache(R):
+    """20000 units of 5 tokens: every call, against the oracle at a few of them."""
+    B, Hkv, G, d, n = 4, 5000, 2, 64, 5
+    k, v = T.keys((B, Hkv, 5, d), 1, "bf16"), T.rand((B, Hkv, 5, d), 2, "bf16")
+    cfg = R.Config(head_dim=d, n_q_heads=G * Hkv, n_kv_heads=Hkv, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, 8, B, max_queries=B * n)
+    kv4.recsa_kv4_build(k.cuda(), v.cuda(), [5, 5, 4, 5])
+    kv4.recsa_kv4_append(k[:, :, :1].contiguous().cuda(), v[:, :, :1].contiguous().cuda())
+    Q = T.rand((B, n, G * Hkv, d), 3, "bf16")
+    out = kv4.prefill(Q.cuda(), accumulate_rows=n)
+    dec = kv4.decode(Q[:, 0].contiguous().cuda(), accumulate=True)
+    w = kv4.weights()[:, :, :6].double().sum(-1)
+    assert (w - (n + 1) * G).abs().max() <= 2.0 ** -17 * (n + 1) * G
+    kept = kv4.weights().clone()
+    kv4.recsa_kv4_evict(4, 1, 1)
+    for b, h in [(0, 0), (1, 4999), (2, 2500), (3, 17), (3, 4999)]:
+        u = T.O.Unit(d)
+        L = 4 if b == 2 else 5
+        u.append(T.np64(k[b, h, :L]), T.np64(v[b, h, :L]))
+        u.append(T.np64(k[b, h, :1]), T.np64(v[b, h, :1]))
+        for i in range(n):
+            qs = T.np64(Q[b, i, h * G:(h + 1) * G])
+            floor = T.bound_of(u, qs, "bf16", True)[1]
+            T.check_rows(out[b, i, h * G:(h + 1) * G], u.attend(qs, u.seen - n + i), floor, "bf16", (b, h, i))
+        qs = T.np64(Q[b, 0, h * G:(h + 1) * G])
+        T.check_rows(dec[b, h * G:(h + 1) * G], u.attend(qs, u.seen), T.bound_of(u, qs, "bf16")[1], "bf16", (b, h))
+        u.w = T.np64(kept[b, h, :L + 1])
+        u.evict(4, 1, 1)
+        assert kv4.positions()[b, h, :4].tolist() == u.pos.tolist(), (b, h)
+    assert kv4.lengths().tolist() == [4] * 4 and kv4.recsa_kv4_get_status() == R.RECSA_OK
