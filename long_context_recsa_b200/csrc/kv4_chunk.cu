@@ -33,6 +33,10 @@
 // asked into L2 ahead (+10%), registers shared out by role so that 64 scores stay over the
 // maximum (408), everything unrolled (instruction cache).
 //
+// (O stays in TMEM over a CTA's share of a unit, and the products' accumulators do not round to
+// nearest: over 885 tiles, 7080 products, the output shrank by 1.0e-4 of itself, over 3500 it
+// would be 4e-4, beside 1.66e-3 from its own rounding.)
+//
 // All tiles of all units (sequence, KV head, block of rows) form one list, cut evenly over
 // the CTAs.  Tiles behind a block's last position are left out where slots are positions
 // (nothing was evicted).  A unit that is cut leaves partial results (O, m, sum of P), which
@@ -936,78 +940,120 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
     }
 }
 
-// 32 rows of a unit of a wide sequence (kv4_is_wide), in plain fp32: a lane a row.  Tiles of 16
-// tokens: a warp forms the scores of two, then every warp the probabilities (the same ones) and
+// 32 rows of a unit of a wide sequence (kv4_is_wide), in plain fp32: a lane a row.  Tiles of 32
+// tokens: a warp forms the scores of four, then every warp the probabilities (the same ones) and
 // its eighth of the output's dims; tokens that a row does not see are left out there, as a NaN
-// must not reach it.  Such data is not expected, so this is short rather than fast, and stands in
-// the join's launch: a launch of the other attention kernel cost every call 4 to 6 us.
-constexpr int kWideTok = 16;
+// must not reach it.  The next tile's codes are on their way meanwhile.  Such data is not
+// expected, so this is short rather than fast, and stands in the join's launch: a launch of the
+// other attention kernel cost every call 4 to 6 us.  Measured: 5 rows x 8 sequences at 9001, all
+// wide, 1.2 to 3.0 ms (74 us otherwise), 512 rows at 32768 15 ms (0.35).
+constexpr int kWideTok = 32, kJoinThreads = 256;
 template <int D>
 struct WideSmem {
-    float q[32][D + 1], x[kWideTok][D], s[kWideTok][32];
+    float4 q[32][D / 4 + 1], x[kWideTok][D / 4];
+    float s[kWideTok][32];
     int32_t pos[kWideTok];
 };
 template <int D>
 __device__ __noinline__ void wide_rows(WideSmem<D>& sm, const Kv4View& c, const Kv4Query& qv, int u,
                                        int rel, int rows) {
-    constexpr int E = D / 8;
+    constexpr int E = D / 8, NW = kWideTok * (D / 8) / kJoinThreads;   // words of codes a thread
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = u / c.Hkv, h = u % c.Hkv;
     const int n_b = qv.counts ? qv.counts[b] : qv.n;
     const int row = qv.i0 * c.G + rel + lane, row_end = qv.i0 * c.G + rows;
     const int i = row / c.G, g = row % c.G;
     const int64_t L = c.len[b], at = (((int64_t)b * qv.n + i) * c.Hq + h * c.G + g) * D;
-    const int lim = row < row_end ? (int)(c.seen[b] - n_b + i) : -1;
-    for (int d = warp; d < D; d += 8)
-        sm.q[lane][d] = row < row_end ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(qv.q)[at + d])
-                                      : 0.0f;
-    auto load = [&](const uint8_t* codes, const uint32_t* pars, int64_t t0) {
-        for (int k = threadIdx.x; k < kWideTok * (D / 8); k += 256) {
-            const int r = k / (D / 8), w = k % (D / 8);
-            const int64_t slot = u * c.R + t0 + r;   // (R is a multiple of whole tiles)
-            const uint32_t code = reinterpret_cast<const uint32_t*>(codes)[slot * (D / 8) + w];
-            const uint32_t par = pars[slot * (D / 32) + w / 4];
-#pragma unroll 2
-            for (int e = 0; e < 8; ++e)
-                sm.x[r][w * 8 + e] = fmaf(kv4_step(par), (float)((code >> (4 * e)) & 15u), kv4_off(par));
+    // (rows that are not there see everything, so that whole tiles are seen by all)
+    const int lim = row < row_end ? (int)(c.seen[b] - n_b + i) : 0x7ffffffe;
+    for (int d = warp * E; d < (warp + 1) * E; ++d)
+        reinterpret_cast<float*>(sm.q[lane])[d] =
+            row < row_end ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(qv.q)[at + d]) : 0.0f;
+    struct Raw { uint32_t code, par; } k[NW], v[NW];
+    int32_t pos = 0x7fffffff;
+    auto ask = [&](int64_t t0) {
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int y = threadIdx.x + j * kJoinThreads;
+            const int64_t slot = u * c.R + t0 + y / (D / 8);     // (R is a multiple of whole tiles)
+            const int64_t word = slot * (D / 8) + y % (D / 8), group = slot * (D / 32) + y % (D / 8) / 4;
+            k[j] = {reinterpret_cast<const uint32_t*>(c.kc)[word], c.kp[group]};
+            v[j] = {reinterpret_cast<const uint32_t*>(c.vc)[word], c.vp[group]};
+        }
+        if (threadIdx.x < kWideTok)
+            pos = t0 + threadIdx.x < L ? c.pos[u * c.R + t0 + threadIdx.x] : 0x7fffffff;
+    };
+    auto put = [&](const Raw (&raw)[NW]) {
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int y = threadIdx.x + j * kJoinThreads;
+            const float s = kv4_step(raw[j].par), lo = kv4_off(raw[j].par);
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = fmaf(s, (float)((raw[j].code >> (4 * e)) & 15u), lo);
+            float4* to = &sm.x[y / (D / 8)][y % (D / 8) * 2];
+            to[0] = make_float4(z[0], z[1], z[2], z[3]);
+            to[1] = make_float4(z[4], z[5], z[6], z[7]);
         }
     };
     const float scale = c.scale * 1.4426950408889634f;
     float o[E], m = kKv4MinLog2, l = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    ask(0);
 #pragma unroll 1
     for (int64_t t0 = 0; t0 < L; t0 += kWideTok) {
         __syncthreads();
-        load(c.kc, c.kp, t0);
-        if (threadIdx.x < kWideTok)
-            sm.pos[threadIdx.x] = t0 + threadIdx.x < L ? c.pos[u * c.R + t0 + threadIdx.x] : 0x7fffffff;
+        put(k);
+        if (threadIdx.x < kWideTok) sm.pos[threadIdx.x] = pos;
         __syncthreads();
-#pragma unroll 1
-        for (int k = 0; k < kWideTok / 8; ++k) {
-            float s = 0.0f;
-#pragma unroll 8
-            for (int d = 0; d < D; ++d) s = fmaf(sm.q[lane][d], sm.x[warp * (kWideTok / 8) + k][d], s);
-            sm.s[warp * (kWideTok / 8) + k][lane] = s * scale;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int d = 0; d < D / 4; ++d) {
+            const float4 q = sm.q[lane][d];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = sm.x[warp * 4 + j][d];
+                s[j] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, s[j]))));
+            }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sm.s[warp * 4 + j][lane] = s[j] * scale;
         __syncthreads();
-        load(c.vc, c.vp, t0);
+        put(v);
+        if (t0 + kWideTok < L) ask(t0 + kWideTok);
         __syncthreads();
         float mn = m;
-#pragma unroll 4
-        for (int k = 0; k < kWideTok; ++k)
-            if (sm.pos[k] <= lim) mn = fmaxf(mn, sm.s[k][lane]);
+        bool all = true;
+#pragma unroll 8
+        for (int j = 0; j < kWideTok; ++j) {
+            const bool sees = sm.pos[j] <= lim;
+            all &= sees;
+            if (sees) mn = fmaxf(mn, sm.s[j][lane]);
+        }
         const float f = ex2(m - mn);
         m = mn;
         l *= f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll 1
-        for (int k = 0; k < kWideTok; ++k) {
-            if (sm.pos[k] > lim) continue;
-            const float p = ex2(sm.s[k][lane] - m);
+        auto add = [&](int j) {
+            const float p = ex2(sm.s[j][lane] - m);
             l += p;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(p, sm.x[k][warp * E + e], o[e]);
+            for (int e = 0; e < E; e += 4) {
+                const float4 x = sm.x[j][(warp * E + e) / 4];
+                o[e] = fmaf(p, x.x, o[e]);
+                o[e + 1] = fmaf(p, x.y, o[e + 1]);
+                o[e + 2] = fmaf(p, x.z, o[e + 2]);
+                o[e + 3] = fmaf(p, x.w, o[e + 3]);
+            }
+        };
+        if (__all_sync(kFull, all)) {
+#pragma unroll 8
+            for (int j = 0; j < kWideTok; ++j) add(j);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kWideTok; ++j)
+                if (sm.pos[j] <= lim) add(j);
         }
     }
     if (row >= row_end) return;
@@ -1021,7 +1067,7 @@ __device__ __noinline__ void wide_rows(WideSmem<D>& sm, const Kv4View& c, const 
 // Joins the parts of the units that were cut.  Grid: x = 32 rows, y = unit; a lane a row, a
 // warp some of the 8-dim pieces.
 template <int D>
-__global__ void __launch_bounds__(256, 3) kv4_join_kernel(const __grid_constant__ Kv4View c,
+__global__ void __launch_bounds__(kJoinThreads, 3) kv4_join_kernel(const __grid_constant__ Kv4View c,
                                                           const __grid_constant__ Kv4Query qv,
                                                           Kv4Scratch sc, int RB, int ctas) {
     __shared__ ChunkPlan pl;
@@ -1099,8 +1145,8 @@ cudaError_t chunk_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& s
         ? kv4_launch(kv4_chunk_kernel<D, true>, dim3(kChunkGrid), kChunkThreads, smem, s, c, qv, sc)
         : kv4_launch(kv4_chunk_kernel<D, false>, dim3(kChunkGrid), kChunkThreads, smem, s, c, qv, sc);
     if (e != cudaSuccess) return e;
-    return kv4_launch(kv4_join_kernel<D>, dim3((unsigned)((rows + 31) / 32), (unsigned)(c.B * c.Hkv)), 256,
-                      0, s, c, qv, sc, RB, kChunkGrid);
+    return kv4_launch(kv4_join_kernel<D>, dim3((unsigned)((rows + 31) / 32), (unsigned)(c.B * c.Hkv)),
+                      kJoinThreads, 0, s, c, qv, sc, RB, kChunkGrid);
 }
 
 }  // namespace
