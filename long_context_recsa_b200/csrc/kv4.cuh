@@ -58,6 +58,7 @@ struct Kv4Source {
 struct Kv4Scratch {
     float* part;             // [2 * grid][rows a block][D + 2] split-softmax partials (both kernels')
     uint32_t* ucnt;          // [3 * grid] arrivals at the joins of split units (left at 0)
+    float4* sum;             // kv4_launch_chunk: [grid][2][D / 4][128] sums of O, in large caches
     float2* stat;            // [U][rows] a row's reference m (log2 units) and 1 / sum of 2^(score - m)
 };
 
@@ -87,6 +88,7 @@ cudaError_t kv4_prepare_attend(int dtype, int D);
 cudaError_t kv4_launch_attend(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& sc,
                               const Kv4Maps& maps, int chunk, int dtype, cudaStream_t s);
 size_t kv4_chunk_part_floats(int D, int rows);          // the same for kv4_launch_chunk
+size_t kv4_chunk_sum_floats(int D, int64_t R);          // floats of Kv4Scratch::sum
 cudaError_t kv4_prepare_chunk(int D);
 // bf16 with more than 8 rows a KV head: tensor-core products over blocks of rows, of keys and
 // values as fp16; in fp32 for sequences whose magnitudes span more than that holds (wide)

@@ -17,7 +17,7 @@ struct Kv4Layout {
     int D, G, esize;
     int64_t R, U;
     size_t o_kc, o_vc, o_kp, o_vp, o_pos, o_w, cache_bytes;
-    size_t o_status, o_done, o_len, o_seen, o_kmax, o_vmax, o_kmin, o_vmin, o_wide, o_ucnt, o_stat, o_part, o_lists, ws_bytes;
+    size_t o_status, o_done, o_len, o_seen, o_kmax, o_vmax, o_kmin, o_vmin, o_wide, o_ucnt, o_stat, o_part, o_sum, o_lists, ws_bytes;
 };
 
 // Rows (chunk rows times heads of a group) of one wave and KV head that kv4_launch_chunk takes:
@@ -71,12 +71,14 @@ recsa_status kv4_layout(const recsa_config* c, int64_t cap, int B, int Qmax, Kv4
     L->o_wide = w;   w = up256(w + sizeof(uint32_t) * B);
     L->o_ucnt = w;   w = up256(w + sizeof(uint32_t) * kv4_attend_counters());
     L->o_stat = w;   w = up256(w + sizeof(float2) * (size_t)Qmax * c->n_q_heads);
-    size_t part = kv4_attend_part_floats(L->D);
+    size_t part = kv4_attend_part_floats(L->D), sum = 0;
     if (chunk_on_tensor_cores(c->dtype, Qmax / B * G)) {
+        sum = kv4_chunk_sum_floats(L->D, L->R);
         const size_t p = kv4_chunk_part_floats(L->D, Qmax / B * G);
         if (p > part) part = p;
     }
     L->o_part = w;   w = up256(w + sizeof(float) * part);
+    L->o_sum = w;    w = up256(w + sizeof(float) * sum);
     L->o_lists = w;  w = up256(w + sizeof(int32_t) * rows);
     L->ws_bytes = w;
     return RECSA_OK;
@@ -224,6 +226,7 @@ recsa_status recsa_kv4_init(const recsa_config* cfg, int64_t capacity, int32_t b
     t->sc.ucnt = (uint32_t*)(ws + L.o_ucnt);
     t->sc.stat = (float2*)(ws + L.o_stat);
     t->sc.part = (float*)(ws + L.o_part);
+    t->sc.sum = (float4*)(ws + L.o_sum);
     t->lists = (int32_t*)(ws + L.o_lists);
     OnDevice on(dev);
     const cudaStream_t s = (cudaStream_t)stream;

@@ -24,7 +24,7 @@
 //     fp32 beside it.
 //
 // Precision.  q enters as fp16 scaled by a power of two to [2^10, 2^11): a bf16 q is exact
-// there but for elements below 2^-24 of the row's largest (off by 2^-32 of that).  P' enters as
+// there but for elements below 2^-23 of the row's largest (off by 2^-31 of that).  P' enters as
 // fp16, off by at most 2^-11 relative, less than bf16's own 2^-8 of the output.  fp32 tensors
 // use two fp16 columns a row for q and for P' (high and low part, 22 bits; the low part of P'
 // is scaled by 2^11, so that it keeps its bits where P' itself is below fp16's normal range).
@@ -49,11 +49,12 @@
 // unit cut over several CTAs is joined by the last of each 16 and then by the last of those
 // (one CTA joining all 74 of a unit took longer than the unit).
 //
-// Measured (B200): decode of 4 x 524288 tokens, 8 KV heads, 32 heads, d = 128: 666 us for
-// 2684 MB, 4.0 TB/s, 62% of a plain copy's rate.  Instructions bound it: 480 a warp for 16
-// tokens of K and V, issued in 60% of the cycles, half of them on the pipe of the masks and
-// conversions.  131072 tokens of one sequence: 64 us, of which the start, the plan and the
-// joins are about 20.
+// Measured (B200): decode of 4 x 524288 tokens, 8 KV heads, 32 heads, d = 128: 711 us for
+// 2684 MB, 3.8 TB/s, 58% of a plain copy's rate (699 to 723 from box to box).  540 instructions a
+// warp for 16 tokens of K and V would take 1.2 times the copy's time if one were issued in every
+// cycle; 62% of the cycles issue one and the busiest pipe (masks and conversions) is half used,
+// so what bounds it is the latency of a warp's one chain at four warps a scheduler.  131072
+// tokens of one sequence: 64 us, of which the start, the plan and the joins are about 20.
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -960,9 +961,9 @@ __global__ void __launch_bounds__(kAttendThreads, ctas_per_sm<NCS>()) kv4_attend
 //
 // Registers: fp32 rows take 168 (three CTAs an SM); held to 128, 16 x 3999 took 3 us more.
 //
-// Measured: 32 us for one row of 131072 tokens x 8 KV heads (84 MB of keys, 8 of weights);
-// 128 rows a KV head of 16384 x 8: 88 us a launch, bound by the latency of scores and
-// exponentials at eight warps an SM.
+// Measured: 37 us for one row of 131072 tokens x 8 KV heads (84 MB of keys, 8 of weights); 128
+// rows a KV head of 16384 x 8: 115 us for the sums and 86 us for the weights, bound by the
+// latency of scores and exponentials at eight warps an SM.
 template <int D, int T, bool CHUNK, bool SUMS>
 __global__ void __launch_bounds__(kAttendThreads, T == 2 ? 3 : 4) kv4_weights_kernel(
     Kv4View c, Kv4Query qv, Kv4Scratch sc_, const __grid_constant__ Kv4Maps maps, int first_row,

@@ -33,9 +33,9 @@
 // asked into L2 ahead (+10%), registers shared out by role so that 64 scores stay over the
 // maximum (408), everything unrolled (instruction cache).
 //
-// (O stays in TMEM over a CTA's share of a unit, and the products' accumulators do not round to
-// nearest: over 885 tiles, 7080 products, the output shrank by 1.0e-4 of itself, over 3500 it
-// would be 4e-4, beside 1.66e-3 from its own rounding.)
+// The products' accumulators do not round to nearest: over 7080 products (885 tiles) O shrank by
+// 1.0e-4 of itself.  So a stream adds O to fp32 sums in the workspace every 256 tiles, and O starts
+// from zero again (a cache of 32768 tokens and less never gets there).
 //
 // All tiles of all units (sequence, KV head, block of rows) form one list, cut evenly over
 // the CTAs.  Tiles behind a block's last position are left out where slots are positions
@@ -60,6 +60,7 @@ constexpr uint32_t kNanPar = 0x7fc00000u;   // lo = NaN, s = 0
 constexpr float kUp = 8.0f;               // P is scaled by 2^8, and stays below 2^14
 constexpr float kMostP = 16384.0f;        // P moves the reference where it passes 2^(kUp + 6)
 constexpr float kNoScore = -3e38f;
+constexpr int kFlush = 256;               // tiles of a stream whose products O sums up (a power of two)
 
 template <int D>
 struct ChunkSmem {
@@ -367,6 +368,38 @@ __device__ __noinline__ Moved move_reference(uint32_t ts, uint32_t to, int k, bo
     st_done();
     return {ref, fmaf(l2.x + l2.y, f, sum.x + sum.y)};
 }
+// A row's O of the last kFlush tiles goes to its sums (of the rows of this stream, 128 apart),
+// which are `f` times what is there; f = 0: nothing is there.  (O's products are done, as above.)
+template <int D>
+__device__ __noinline__ void flush_o(uint32_t to, float4* sum, float f) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        float o[32];
+        ld32(to + k, o);
+        ld_done(o);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            float4* s = sum + (k + e) / 4 * kRowsStream;
+            float4 v = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if (f != 0.0f) {
+                const float4 y = *s;
+                v = make_float4(fmaf(f, y.x, v.x), fmaf(f, y.y, v.y), fmaf(f, y.z, v.z), fmaf(f, y.w, v.w));
+            }
+            *s = v;
+        }
+    }
+}
+// Adds f times the sums of dims 32 k .. to the 32 values of O.
+__device__ __forceinline__ void add_sums(float (&o)[32], const float4* sum, float f) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 y = sum[e / 4 * kRowsStream];
+        o[e] = fmaf(f, y.x, o[e]);
+        o[e + 1] = fmaf(f, y.y, o[e + 1]);
+        o[e + 2] = fmaf(f, y.z, o[e + 2]);
+        o[e + 3] = fmaf(f, y.w, o[e + 3]);
+    }
+}
 // Groups of dims in which a token that the row sees holds NaN.
 template <int NG>
 __device__ __noinline__ uint32_t nan_groups(const int32_t* pos, const uint32_t* any,
@@ -645,6 +678,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             const int X = un.X, mine = (X - stream + 1) / 2;
             const bool some = __any_sync(kFull, lim >= 0);
             float ref = kNoScore;      // of the exponent, in the products' units
+            float sum_ref = kNoScore;  // the same of this row's sums of O
+            float4* sum = sc.sum + ((size_t)blockIdx.x * 2 + stream) * (D / 4) * kRowsStream + r;
             float2 l2 = make_float2(0.0f, 0.0f);
             uint32_t nanbits = 0;
             bool ok = true;
@@ -654,6 +689,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                 if (!ok) break;
                 s_parity ^= 1;
                 tc_after();
+                if (some && j > 0 && j % kFlush == 0) {
+                    if (!in_bounds(c.R / kTok > kFlush, c.status)) break;   // (sums are there)
+                    flush_o<D>(to, sum, j > kFlush ? ex2((sum_ref - ref) * rsc) : 0.0f);
+                    sum_ref = ref;
+                }
                 if (some) {
                     const int4 pm = *reinterpret_cast<const int4*>(pos_max[slot]);
                     const uint4 na = *reinterpret_cast<const uint4*>(nan_any[slot]);
@@ -708,6 +748,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             const int64_t cta0 = un.start / quota, cta1 = (un.start + un.tiles - 1) / quota;
             const bool whole = cta0 == cta1;
             const int ev = exponent_of(__uint_as_float(c.vmax[un.u]));
+            const bool sums = mine > kFlush;
+            const float f_sum = ex2((sum_ref - ref) * rsc);
             float f0 = 1.0f, f1 = 0.0f;
             float4* other = reinterpret_cast<float4*>(smem + Sm::kK);   // [D / 4][128]: K is done
             if (!TWO) {
@@ -722,6 +764,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                             float o[32];
                             ld32(to + k, o);
                             ld_done(o);
+                            if (sums) add_sums(o, sum + k / 4 * kRowsStream, f_sum);
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
                                 other[(k + e) / 4 * 128 + r] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -751,6 +794,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
                     float o[32];
                     ld32(to + k, o);
                     ld_done(o);
+                    if (sums) add_sums(o, sum + k / 4 * kRowsStream, f_sum);
                     if (f1 != 0.0f) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -926,8 +970,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(Kv4View c, 
             const std::integral_constant<int, 1> s1;
             ok = qk(s0) && (X < 2 || qk(s1));
             for (int x = 0; ok && x < X; x += 2) {
-                ok = pv(s0, x == 0, x + 2 < X);
-                if (ok && x + 1 < X) ok = pv(s1, x == 0, x + 3 < X);
+                const bool first = (x / 2) % kFlush == 0;   // O was moved to the sums
+                ok = pv(s0, first, x + 2 < X);
+                if (ok && x + 1 < X) ok = pv(s1, first, x + 3 < X);
             }
             if (elect_one()) commit(&bars.o_full);
             __syncwarp();
@@ -1153,6 +1198,10 @@ cudaError_t chunk_impl(const Kv4View& c, const Kv4Query& qv, const Kv4Scratch& s
 
 size_t kv4_chunk_part_floats(int D, int rows) {
     return (size_t)2 * kChunkGrid * chunk_rows(rows) * (D + 2);
+}
+
+size_t kv4_chunk_sum_floats(int D, int64_t R) {
+    return R / kTok > kFlush ? (size_t)kChunkGrid * 2 * kRowsStream * D : 0;
 }
 
 template <int D>

@@ -6,10 +6,11 @@
 // a group (16 dims each), so what is done once a group costs a sixteenth of it a dim, and
 // the group's minimum and maximum take one exchange; arithmetic goes two dims at a time.
 //
-// Measured (B200, 131072 x 8 rows of bf16, d = 128): build 207 us for 705 MB, 3.4 TB/s, bound by
-// instructions (311 a warp for 512 dims, issued in 71% of the cycles); read 105 us for 705
-// MB, 6.7 TB/s.  Fewer or more rows in flight a lane than 2 (433 and 270 us) and another
-// number of CTAs than 4 (231 to 275) were slower.
+// Measured (B200, 131072 x 8 rows of bf16, d = 128): build 214 us for 705 MB, 3.3 TB/s: 314
+// instructions a warp for 512 dims, issued in 70% of the cycles, the busiest pipe (ALU) half used:
+// latency, and the instruction cache.  (Keeping the smallest group beside the largest value costs
+// 6 us of it.)  Fewer or more rows in flight a lane than 2 (433 and 270 us) and another number of
+// CTAs than 4 (231 to 275) were slower.  Read 105 us for 705 MB, 6.7 TB/s.
 #include "kv4.cuh"
 
 namespace recsa {

@@ -265,3 +265,34 @@ def test_bf16_sums_over_a_long_cache_do_not_drift(R):
     own = (want.bfloat16().double() - want).norm()
     assert (out - want).norm() <= (own.square() + (2.0 ** -11 * want.norm()).square()).sqrt()
     assert kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+@pytest.mark.parametrize("Hkv,G,n,L,mean", [(64, 2, 70, 1_000_000, 0.0), (148, 1, 12, 300_001, 0.3), (200, 1, 130, 70_000, 0.0)])
+def test_chunk_sums_over_a_long_cache_do_not_drift(R, Hkv, G, n, L, mean):
+    """Units that lie nearly whole in a CTA (one pair of tensors read by all: strides of 0).  The
+    products' accumulators may lose half a step, 2^-25, a product, over the 2048 products of 256
+    tiles; the outputs' own rounding is unbiased (its mean over 2000 and more outputs is below
+    2^-8 / 3 / 45).  So the outputs' scale is within 2^-13 of the exact one."""
+    d = 64
+    k, v, Q = normal(L, d, n, Hkv * G, 10)
+    k, v, Q = k.bfloat16().cuda(), (v + mean).bfloat16().cuda(), Q.bfloat16().cuda()
+    cfg = R.Config(head_dim=d, n_q_heads=G * Hkv, n_kv_heads=Hkv, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, L, 1, max_queries=n)
+    kv4.recsa_kv4_build(k.expand(1, Hkv, L, d), v.expand(1, Hkv, L, d), [L])
+    out = kv4.prefill(Q[None])[0].double()
+    u = O.Unit(d)
+    u.append(T.np64(k), T.np64(v))
+    K, V = torch.from_numpy(u.k).cuda(), torch.from_numpy(u.v).cuda()
+    at = torch.arange(L, device="cuda")[None] <= L - n + torch.arange(n, device="cuda")[:, None]
+    dot = square = off = own = 0.0
+    for h in (0, Hkv // 2, Hkv - 1):
+        s = (Q[:, h * G].double() @ K.T / d ** 0.5).masked_fill(~at, -float("inf"))
+        want, got = torch.softmax(s, -1) @ V, out[:, h * G]
+        dot += float((got * want).sum())
+        square += float(want.square().sum())
+        off += float((got - want).square().sum())
+        own += float((want.bfloat16().double() - want).square().sum())
+    assert abs(dot / square - 1) <= 2.0 ** -13, dot / square - 1
+    # K, V and P as fp16 are off by 2^-11 each, independently
+    assert off <= own + 3 * 2.0 ** -22 * square, ((off / square) ** 0.5, (own / square) ** 0.5)
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
