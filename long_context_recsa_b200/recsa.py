@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, importing this module fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass, field
@@ -412,6 +413,7 @@ class RecsaKV4:
         # fixed for the handle's life, so that a call of a few microseconds forms none of it
         self._dtype = cfg.torch_dtype
         self._index = self.device.index
+        self._empty = functools.partial(torch.empty, dtype=self._dtype, device=self.device)
         self._q_shape = (batch, cfg.n_q_heads, cfg.head_dim)
         rows = (batch, cfg.n_kv_heads, self.info.rows)
         self._positions = self._table(self.cache, self.info.positions, rows, torch.int32)
@@ -530,8 +532,8 @@ class RecsaKV4:
 
     def read(self, start: int, n: int, stream=None):
         shape = (self.batch, self.cfg.n_kv_heads, n, self.cfg.head_dim)
-        k, v = (self._new(lambda x: torch.empty(x, dtype=self.cfg.torch_dtype, device=self.device),
-                          shape, stream) for _ in range(2))
+        k = self._new(self._empty, shape, stream)
+        v = self._new(torch.empty_like, k, stream)
         self.recsa_kv4_read(start, n, k, v, stream)
         return k, v
 
