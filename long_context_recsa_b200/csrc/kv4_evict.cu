@@ -283,12 +283,21 @@ __global__ void __launch_bounds__(kEvictThreads) kv4_evict_kernel(Kv4View c, int
 
 namespace {
 
-// CTAs of a unit, by the capacity (the length is known on the device only).  4097 of 4102
-// slots: one CTA 16 us, a cluster of four 19 us; 10240 of 10245: one 41 us, eight 23 us.
-int evict_cluster(int64_t cap) { return cap <= 6144 ? 1 : 8; }
+// CTAs of a unit: one or a cluster of eight, by the capacity (the length is known on the device
+// only) and by how often the clusters of all units fill the GPU.  One CTA / eight, us, where one
+// row goes and where a fifth of them go:
+//     units  4096           8192           16384           32768            131072
+//         8  16/20  28/21   21/23  43/25   29/23   70/28   43/25  154/39    301/37  786/100
+//        32  18/25  29/27   21/26  49/31   31/29   87/39   44/32  166/53    303/57  854/160
+//       128  18/82  33/91   23/88  57/109  31/92  107/139  45/105 205/202
+int evict_cluster(const Kv4View& c) {
+    constexpr int kResident = 2 * 148;       // CTAs of this kernel at once
+    const int64_t waves = ((int64_t)c.B * c.Hkv * 8 + kResident - 1) / kResident;
+    return c.cap <= 6144 * waves && c.cap <= kEvictKeys ? 1 : 8;
+}
 
-size_t evict_smem(int64_t cap) {
-    const int64_t seg = ((cap + evict_cluster(cap) - 1) / evict_cluster(cap) + 127) / 128 * 128;
+size_t evict_smem(int64_t cap, int ctas) {
+    const int64_t seg = ((cap + ctas - 1) / ctas + 127) / 128 * 128;
     return sizeof(uint32_t) * (size_t)(seg < kEvictKeys ? seg : kEvictKeys);
 }
 
@@ -297,7 +306,7 @@ cudaError_t evict_impl(const Kv4View& c, int64_t budget, int64_t n_first, int64_
                        int32_t* lists, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
-    const int cs = evict_cluster(c.cap);
+    const int cs = evict_cluster(c);
     at[0] = pdl_attribute();
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)cs;
@@ -305,7 +314,7 @@ cudaError_t evict_impl(const Kv4View& c, int64_t budget, int64_t n_first, int64_
     at[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(c.B * c.Hkv * cs));
     cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = evict_smem(c.cap);
+    cfg.dynamicSmemBytes = evict_smem(c.cap, cs);
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 2;

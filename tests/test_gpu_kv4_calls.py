@@ -159,3 +159,40 @@ def test_many_heads_of_a_short_cache(R):
         u.evict(4, 1, 1)
         assert kv4.positions()[b, h, :4].tolist() == u.pos.tolist(), (b, h)
     assert kv4.lengths().tolist() == [4] * 4 and kv4.recsa_kv4_get_status() == R.RECSA_OK
+
+
+@pytest.mark.parametrize("B,Hkv,L,cap,budget", [
+    (16, 8, 7000, 7100, 6000), (2, 3, 7000, 7100, 6999), (64, 16, 3000, 45000, 1500), (5, 8, 20000, 20001, 4097),
+    (64, 8, 9000, 50000, 8999)])
+def test_evict_of_many_and_few_units(R, B, Hkv, L, cap, budget):
+    """One CTA a unit and a cluster, by the units and the capacity; ragged lengths, many ties."""
+    first, recent = 5, 100
+    lengths = [L - 37 * (b % 5) for b in range(B)]
+    cfg = R.Config(head_dim=64, n_q_heads=Hkv, n_kv_heads=Hkv, dtype="bf16")
+    kv4 = R.RecsaKV4(cfg, cap, B)
+    x = torch.zeros(1, 1, L, 64, dtype=torch.bfloat16, device="cuda").expand(B, Hkv, L, 64)
+    kv4.recsa_kv4_build(x, x, lengths)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = (torch.rand(B, Hkv, L, generator=g, device="cuda") * 500).floor()
+    at, Ls = torch.arange(L, device="cuda"), torch.tensor(lengths, device="cuda")[:, None]
+    there = at < Ls
+    w = torch.where(there[:, None], w, 0.0)
+    kv4.weights()[:, :, :L] = w
+    kv4.recsa_kv4_evict(budget, first, recent)
+    safe = (at < first) | (at >= Ls - recent)
+    key = torch.where(safe[:, None], torch.inf, w)
+    key = torch.where(there[:, None], key, -1.0)
+    order = torch.sort(key, dim=-1, descending=True, stable=True).indices[..., :budget]
+    kept = torch.zeros(B, Hkv, L, dtype=torch.bool, device="cuda").scatter_(2, order, True)
+    pos = kv4.positions()
+    for b in range(B):
+        if lengths[b] <= budget:
+            assert torch.equal(pos[b, :, :lengths[b]], at[:lengths[b]].int().expand(Hkv, -1))
+            continue
+        for h in range(0, Hkv, 3):
+            want = torch.arange(budget, device="cuda")
+            want[~kept[b, h, :budget]] = at[budget:][kept[b, h, budget:]]
+            assert torch.equal(pos[b, h, :budget].long(), want), (b, h)
+            assert torch.equal(kv4.weights()[b, h, :budget], w[b, h, want])
+    assert kv4.lengths().tolist() == [min(x, budget) for x in lengths]
+    assert kv4.recsa_kv4_get_status() == R.RECSA_OK
