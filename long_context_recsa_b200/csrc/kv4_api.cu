@@ -21,7 +21,14 @@ struct Kv4Layout {
 };
 
 // Rows (chunk rows times heads of a group) of one wave and KV head that kv4_launch_chunk takes:
-// what does not fit the 8 columns of the other kernel's narrowest form, in bf16.
+// what does not fit the 8 columns of the other kernel's narrowest form, in bf16.  Chunk kernel /
+// the other with a block for every 8 rows, us, 8 KV heads, d = 128:
+//     sequences x tokens   12 rows    16         20         32         64
+//     1 x 1500             23/25      25/27      26/26      27/29      29/28
+//     1 x 9000             46/33      47/34      48/36      50/42      53/49
+//     8 x 9000             85/78      87/78      92/104     94/131     94/236
+//     1 x 131072           142/123    141/124    148/171    145/218    148/407
+//     4 x 131072           403/407    407/408    409/598    410/789    412/1548
 bool chunk_on_tensor_cores(int dtype, int rows) { return dtype == RECSA_BF16 && rows > 8; }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
